@@ -503,6 +503,121 @@ lowram_status lowram_encode(const lowram_config* cfg, int32_t n_resid, const voi
                             const void* w2, const lowram_encode_dst* dst, void* workspace,
                             uint64_t workspace_bytes, lowram_stream stream);
 
+/* ------------------------------------------------------------- quantised KV cache
+ *
+ * A paged KV cache held in 4 or 8 bits: tokens are quantised as they are written, and decode
+ * attends over the codes without a dequantised copy -- over whole sequences, or over the pages
+ * that a cheap score selects for each query.  It is the form a low-rank cache is weighed
+ * against, and the one for layers whose keys have no low-rank basis.  The pages have no
+ * counterpart beyond the composition of LowRAM with quantisation.
+ *
+ * Format.  A row (one token of one layer and KV head, K or V) is cut into groups of 64
+ * channels.  With b bits, per group:
+ *     lo = fp16(min x),   s = fp16(fp32((max x - min x) / (2^b - 1))),
+ *     n  = clamp(round-half-even((x - lo) / s), 0, 2^b - 1)   (n = 0 when s = 0),
+ *     and the group stands for  xhat = lo + s * n.
+ * Values must be finite and within fp16's range: a group that holds another value reads back
+ * as non-finite values (it does not disturb other groups).
+ *
+ * A pool holds n_pages pages of `page` tokens for every layer; sequence b's i-th page is
+ * table[b][i], the same for all layers (table NULL: page b * max_pages + i).  Sequences may
+ * share pages that neither of them writes.  A page's mean key (the mean over its `page`
+ * tokens of khat) is stored by the write that fills the page's last slot.
+ *
+ * All entry points: caller-owned DEVICE arrays, stream-ordered, no allocation, no host
+ * synchronisation, capturable.  A page id outside [0, n_pages) and a length, position or count
+ * outside its range (read on the device) never become an access: such tokens are left out
+ * (a read gives zeros for them, attention masks them, a length above max_pages * page counts as
+ * that many tokens) and the error word records it. */
+typedef struct {
+  int32_t batch;       /* B: sequences */
+  int32_t n_layers;    /* L: layers of the pool */
+  int32_t n_kv_heads;  /* Hkv */
+  int32_t n_q_heads;   /* Hq, a multiple of Hkv, at most 16 query heads per KV head */
+  int32_t head_dim;    /* d: 64, 128 or 256 */
+  int32_t page;        /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t n_pages;     /* P: pages of the pool (per layer) */
+  int32_t max_pages;   /* pages of a sequence's table row; at most 16384 */
+  int32_t bits;        /* 4 or 8 */
+  int32_t dtype;       /* lowram_dtype of k, v, q and out */
+} lowram_kvq_config;
+
+/* The cache's arrays (DEVICE, 16-byte aligned; G = d / 64):
+ *   k_code, v_code   [L][P][Hkv][page][d * bits / 8] bytes.  A row is 8 G cells of 8 codes:
+ *                    channel 64 g + 8 w + i is code i of cell w * G + g (4 bits: byte i / 2 of
+ *                    the cell, low nibble first).
+ *   k_scale, v_scale [L][P][Hkv][page][G][2] fp16: (s, lo).
+ *   k_mean           [L][P][Hkv][d] bf16; may be NULL when lowram_kvq_sparse_attn is not used.
+ *   table            [B][max_pages] int32, or NULL.
+ *   err              one uint32, or NULL: bit 0 a bad page id, bit 1 a bad length, position or
+ *                    count.  Bits are only ever added; the caller clears them. */
+typedef struct {
+  void* k_code;
+  void* k_scale;
+  void* v_code;
+  void* v_scale;
+  void* k_mean;
+  const int32_t* table;
+  uint32_t* err;
+} lowram_kvq_cache;
+
+/* Bytes of one token of one layer and KV head (codes and scales, K and V); 0 for a bad config.
+ * Host only. */
+uint64_t lowram_kvq_token_bytes(const lowram_kvq_config* cfg);
+
+/* Quantise new tokens into layers [layer0, layer0 + n_layers) of the cache.
+ *   k, v      dt, DEVICE: element (layer, sequence, token, head, channel) of k is at
+ *             k[layer * k_stride[0] + sequence * k_stride[1] + token * k_stride[2]
+ *               + head * k_stride[3] + channel] (strides in elements; slices of a fused
+ *             projection are read in place); v likewise.  Base and strides are multiples of 16
+ *             bytes, strides not negative.
+ *   pos       [B] int32, DEVICE: the slot in its sequence of each sequence's first new token.
+ *   count     [B] int32, DEVICE, or NULL: how many of the n_new tokens of sequence b are
+ *             written (NULL: all).
+ * A page whose last slot is written gets its mean from all its tokens, earlier ones included:
+ * write a sequence in order, from its end on (tokens dropped from the end may be written anew).
+ * Two sequences of a call may not write into the same page. */
+lowram_status lowram_kvq_write(const lowram_kvq_config* cfg, const lowram_kvq_cache* cache, int32_t layer0,
+                               int32_t n_layers, int32_t n_new, const void* k, const int64_t* k_stride,
+                               const void* v, const int64_t* v_stride, const int32_t* pos, const int32_t* count,
+                               lowram_stream stream);
+
+/* Read tokens back: k_out, v_out take xhat (rounded once to dt) of tokens pos[b] + i,
+ * i < min(count[b], n_tok), addressed like k and v of lowram_kvq_write (strides of axes longer
+ * than one may not be 0); the rows behind are left as they were. */
+lowram_status lowram_kvq_read(const lowram_kvq_config* cfg, const lowram_kvq_cache* cache, int32_t layer0,
+                              int32_t n_layers, int32_t n_tok, void* k_out, const int64_t* k_stride, void* v_out,
+                              const int64_t* v_stride, const int32_t* pos, const int32_t* count,
+                              lowram_stream stream);
+
+/* Bytes of the workspace lowram_kvq_decode_attn needs for calls of up to n_layers layers and
+ * n_q query tokens (0 for a bad config).  Host only. */
+uint64_t lowram_kvq_workspace_bytes(const lowram_kvq_config* cfg, int32_t n_layers, int32_t n_q);
+
+/* Attention of the last n_q tokens of every sequence over the sequence (causal among them):
+ *   q, out  [n_layers][B][n_q][Hq][d] dt, DEVICE, 16-byte aligned; 1 <= n_q <= 16;
+ *   lens    [B] int32, DEVICE: tokens held by each sequence, its n_q query tokens included.
+ * Query i attends tokens t < lens[b] - n_q + i + 1:  o = softmax_t(q . khat_t / sqrt(d)) vhat_t,
+ * 0 for a query without tokens.  fp32 (or wider) logits, softmax statistics and sums; BF16
+ * calls round the softmax weights to fp16 (times the value scale) for the tensor cores.
+ * workspace: lowram_kvq_workspace_bytes bytes, 16-byte aligned, all zero before its first use;
+ * a call leaves it ready for the next one.  Calls that overlap on the GPU need workspaces of
+ * their own. */
+lowram_status lowram_kvq_decode_attn(const lowram_kvq_config* cfg, const lowram_kvq_cache* cache, int32_t layer0,
+                                     int32_t n_layers, int32_t n_q, const void* q, const int32_t* lens, void* out,
+                                     void* workspace, uint64_t workspace_bytes, lowram_stream stream);
+
+/* The same over selected pages only.  With lim = lens[b] - n_q + i + 1 and c* = (lim - 1) / page,
+ * query i of KV head h attends the tokens t < lim of its newest page c* and of the
+ * min(top_k - 1, c*) pages c < c* with the highest score  sum_{j in h's group} q_j . k_mean[c]
+ * (computed in 64 bits; equal scores go to the lower page, NaN counts as -infinity).
+ *   sel  [n_layers][B][n_q][Hkv][top_k] int32, DEVICE, or NULL: the pages' places in the
+ *        sequence, ascending, then -1.
+ * 1 <= top_k <= 512.  Needs no workspace. */
+lowram_status lowram_kvq_sparse_attn(const lowram_kvq_config* cfg, const lowram_kvq_cache* cache, int32_t layer0,
+                                     int32_t n_layers, int32_t n_q, int32_t top_k, const void* q,
+                                     const int32_t* lens, void* out, int32_t* sel, lowram_stream stream);
+
 /* ------------------------------------------------------------------- test hooks
  *
  * For tests of the failure paths only; a deployment never calls these.  They make a failure

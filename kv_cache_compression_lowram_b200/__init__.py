@@ -10,6 +10,8 @@ Entry points keep the C names: ``lowram_cache_create``, ``lowram_decode_attn``,
 ``lowram_config_bytes``, ``lowram_cache_validate``, ``lowram_cache_destroy``,
 ``lowram_dense_kv_bytes``, ``lowram_cache_set_stage_events``,
 ``lowram_cache_last_launches``, ``lowram_cache_last_path``.  ``LowramCache`` wraps a handle.
+The quantised KV cache (``lowram_kvq_write``, ``lowram_kvq_read``, ``lowram_kvq_decode_attn``,
+``lowram_kvq_sparse_attn``) works on the caller's arrays; ``LowramKvq`` keeps them together.
 """
 
 from __future__ import annotations
@@ -28,6 +30,8 @@ __all__ = [
     "lowram_cache_view", "lowram_cache_append", "lowram_cache_repack",
     "lowram_encode", "LowramReuse", "lowram_reuse_create", "lowram_reuse_destroy",
     "lowram_decode_attn_reuse", "lowram_reuse_counts_get", "lowram_reuse_view",
+    "lowram_kvq_token_bytes", "lowram_kvq_workspace_bytes", "lowram_kvq_write", "lowram_kvq_read",
+    "lowram_kvq_decode_attn", "lowram_kvq_sparse_attn", "kvq_config_struct", "LowramKvq",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblowram.so")
@@ -63,6 +67,17 @@ class LowramBytesC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in (
         "coeff", "basis", "predictor", "summary", "residual", "index", "tail", "total",
         "dense_equiv")]
+
+
+class LowramKvqConfigC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "n_layers", "n_kv_heads", "n_q_heads", "head_dim", "page", "n_pages", "max_pages",
+        "bits", "dtype")]
+
+
+class LowramKvqCacheC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_code", "k_scale", "v_code", "v_scale", "k_mean", "table", "err")]
 
 
 _LIB = None
@@ -116,6 +131,16 @@ def lib() -> ctypes.CDLL:
         "lowram_reuse_counts_get": (I32, [P, ctypes.POINTER(LowramReuseCountsC), P]),
         "lowram_reuse_view": (I32, [P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P),
                                     ctypes.POINTER(I64)]),
+        "lowram_kvq_token_bytes": (U64, [ctypes.POINTER(LowramKvqConfigC)]),
+        "lowram_kvq_workspace_bytes": (U64, [ctypes.POINTER(LowramKvqConfigC), I32, I32]),
+        "lowram_kvq_write": (I32, [ctypes.POINTER(LowramKvqConfigC), ctypes.POINTER(LowramKvqCacheC), I32, I32, I32,
+                                   P, ctypes.POINTER(I64), P, ctypes.POINTER(I64), P, P, P]),
+        "lowram_kvq_read": (I32, [ctypes.POINTER(LowramKvqConfigC), ctypes.POINTER(LowramKvqCacheC), I32, I32, I32,
+                                  P, ctypes.POINTER(I64), P, ctypes.POINTER(I64), P, P, P]),
+        "lowram_kvq_decode_attn": (I32, [ctypes.POINTER(LowramKvqConfigC), ctypes.POINTER(LowramKvqCacheC), I32, I32,
+                                         I32, P, P, P, P, U64, P]),
+        "lowram_kvq_sparse_attn": (I32, [ctypes.POINTER(LowramKvqConfigC), ctypes.POINTER(LowramKvqCacheC), I32, I32,
+                                         I32, I32, P, P, P, P, P]),
         "lowram_debug_set_wait_limit": (I32, [P, I64]),
         "lowram_debug_fail_alloc": (None, [I32]),
         "lowram_status_string": (ctypes.c_char_p, [I32]),
@@ -624,3 +649,251 @@ class LowramCache:
             self.close()
         except Exception:
             pass
+
+
+# --------------------------------------------------------------- quantised KV cache
+
+def kvq_config_struct(cfg) -> LowramKvqConfigC:
+    """C config of a quantised cache from an object or dict with the ``lowram.h`` field names
+    (``dtype`` may be "f32"/"bf16" or 0/1)."""
+    if isinstance(cfg, LowramKvqConfigC):
+        return cfg
+    c = LowramKvqConfigC()
+    for n, _ in LowramKvqConfigC._fields_:
+        v = _get(cfg, n)
+        setattr(c, n, {"f32": 0, "bf16": 1}[v] if isinstance(v, str) else int(v))
+    return c
+
+
+def _kvq_layouts(c) -> dict:
+    import torch
+    lead, d = (c.n_layers, c.n_pages, c.n_kv_heads), c.head_dim
+    return {"k_code": (lead + (c.page, d * c.bits // 8), torch.uint8),
+            "k_scale": (lead + (c.page, d // 64, 2), torch.float16),
+            "v_code": (lead + (c.page, d * c.bits // 8), torch.uint8),
+            "v_scale": (lead + (c.page, d // 64, 2), torch.float16),
+            "k_mean": (lead + (d,), torch.bfloat16),
+            "table": ((c.batch, c.max_pages), torch.int32),
+            "err": ((1,), torch.int32)}
+
+
+def _kvq_cache_struct(c, arrays) -> LowramKvqCacheC:
+    """Pointers of the caller's tensors, after a check of their types, shapes and device."""
+    if isinstance(arrays, LowramKvqCacheC):
+        return arrays
+    out = LowramKvqCacheC()
+    dev = None
+    for name, (shape, dtype) in _kvq_layouts(c).items():
+        try:
+            t = _get(arrays, name)
+        except (AttributeError, KeyError):
+            t = None
+        if t is None:
+            if name in ("k_mean", "table", "err"):
+                continue
+            raise ValueError(f"{name} is missing")
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+        dev = t.device
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {dtype} of shape {shape}, not {t.dtype} of {tuple(t.shape)}")
+        setattr(out, name, _ptr(t))
+    return out
+
+
+def _kvq_call(fn, where, device, stream, *args) -> None:
+    """Call `fn` with the data's device current, on `stream` or that device's current stream."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+            st = fn(*args, s)
+    if st:
+        _check(st, where)
+
+
+def _kvq_dtype(c):
+    import torch
+    return torch.float32 if c.dtype == 0 else torch.bfloat16
+
+
+def _kvq_rows(c, t, name, n_layers=None, n=None):
+    """(pointer, strides) of a [n_layers][B][n][Hkv][d] tensor with contiguous rows."""
+    if t.dim() != 5 or t.shape[1] != c.batch or t.shape[3] != c.n_kv_heads or t.shape[4] != c.head_dim \
+            or (n_layers is not None and t.shape[0] != n_layers) or (n is not None and t.shape[2] != n):
+        raise ValueError(f"{name} must be [n_layers][batch][tokens][n_kv_heads][head_dim]")
+    if not t.is_cuda or t.dtype != _kvq_dtype(c) or t.stride(4) != 1:
+        raise ValueError(f"{name} must be a CUDA tensor of the cache's dtype with contiguous rows")
+    return t.data_ptr(), (ctypes.c_int64 * 4)(*t.stride()[:4])
+
+
+def _kvq_ints(c, t, name, device):
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != c.batch or t.device != device or t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous int32 [batch] tensor on the device of the data")
+    return t.data_ptr()
+
+
+def lowram_kvq_token_bytes(cfg) -> int:
+    return int(lib().lowram_kvq_token_bytes(ctypes.byref(kvq_config_struct(cfg))))
+
+
+def lowram_kvq_workspace_bytes(cfg, n_layers: int, n_q: int) -> int:
+    n = int(lib().lowram_kvq_workspace_bytes(ctypes.byref(kvq_config_struct(cfg)), int(n_layers), int(n_q)))
+    if n == 0:
+        raise LowramError(1, "lowram_kvq_workspace_bytes", lib().lowram_last_error_string().decode())
+    return n
+
+
+def lowram_kvq_write(cfg, arrays, layer0: int, k, v, pos, count=None, stream=None) -> None:
+    """Quantise k, v [n_layers][B][n][Hkv][d] (any strides with contiguous, 16-byte aligned rows)
+    into the cache arrays from slot pos[b] on; count[b] of the n tokens, or all (see lowram.h)."""
+    c = kvq_config_struct(cfg)
+    src = _kvq_cache_struct(c, arrays)
+    kp, ks = _kvq_rows(c, k, "k")
+    vp, vs = _kvq_rows(c, v, "v", k.shape[0], k.shape[2])
+    if v.device != k.device:
+        raise ValueError("k and v must be on one device")
+    _kvq_call(lib().lowram_kvq_write, "lowram_kvq_write", k.device, stream, ctypes.byref(c), ctypes.byref(src), int(layer0),
+              int(k.shape[0]), int(k.shape[2]), kp, ks, vp, vs, _kvq_ints(c, pos, "pos", k.device),
+              _kvq_ints(c, count, "count", k.device))
+
+
+def lowram_kvq_read(cfg, arrays, layer0: int, k_out, v_out, pos, count=None, stream=None) -> None:
+    """Read tokens pos[b] + i, i < count[b] (or all), into k_out, v_out [n_layers][B][n][Hkv][d]."""
+    c = kvq_config_struct(cfg)
+    src = _kvq_cache_struct(c, arrays)
+    kp, ks = _kvq_rows(c, k_out, "k_out")
+    vp, vs = _kvq_rows(c, v_out, "v_out", k_out.shape[0], k_out.shape[2])
+    if v_out.device != k_out.device:
+        raise ValueError("k_out and v_out must be on one device")
+    _kvq_call(lib().lowram_kvq_read, "lowram_kvq_read", k_out.device, stream, ctypes.byref(c), ctypes.byref(src), int(layer0),
+              int(k_out.shape[0]), int(k_out.shape[2]), kp, ks, vp, vs, _kvq_ints(c, pos, "pos", k_out.device),
+              _kvq_ints(c, count, "count", k_out.device))
+
+
+def _kvq_queries(c, q, out):
+    if q.dim() != 5 or q.shape[1] != c.batch or q.shape[3] != c.n_q_heads or q.shape[4] != c.head_dim:
+        raise ValueError("q must be [n_layers][batch][n_q][n_q_heads][head_dim]")
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError("out must be like q")
+    if not q.is_cuda or q.dtype != _kvq_dtype(c):
+        raise ValueError("q must be a CUDA tensor of the cache's dtype")
+    return _ptr(q), _ptr(out)
+
+
+def lowram_kvq_decode_attn(cfg, arrays, layer0: int, q, lens, out, workspace, stream=None) -> None:
+    """Attention of q [n_layers][B][n_q][Hq][d] (each sequence's last n_q tokens) over whole
+    sequences of lens[b] tokens.  ``workspace``: lowram_kvq_workspace_bytes bytes, zeroed once."""
+    c = kvq_config_struct(cfg)
+    src = _kvq_cache_struct(c, arrays)
+    qp, op = _kvq_queries(c, q, out)
+    if workspace.device != q.device:
+        raise ValueError("workspace must be on the device of q")
+    _kvq_call(lib().lowram_kvq_decode_attn, "lowram_kvq_decode_attn", q.device, stream, ctypes.byref(c), ctypes.byref(src),
+              int(layer0), int(q.shape[0]), int(q.shape[2]), qp, _kvq_ints(c, lens, "lens", q.device), op,
+              _ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def lowram_kvq_sparse_attn(cfg, arrays, layer0: int, top_k: int, q, lens, out, sel=None, stream=None) -> None:
+    """The same over each query's newest page and its top_k - 1 best older pages; ``sel``
+    [n_layers][B][n_q][Hkv][top_k] int32 takes their places in the sequence (then -1)."""
+    c = kvq_config_struct(cfg)
+    src = _kvq_cache_struct(c, arrays)
+    qp, op = _kvq_queries(c, q, out)
+    if sel is not None:
+        import torch
+        if tuple(sel.shape) != tuple(q.shape[:3]) + (c.n_kv_heads, int(top_k)) or sel.dtype != torch.int32 \
+                or sel.device != q.device:
+            raise ValueError("sel must be int32 [n_layers][batch][n_q][n_kv_heads][top_k] on the device of q")
+    _kvq_call(lib().lowram_kvq_sparse_attn, "lowram_kvq_sparse_attn", q.device, stream, ctypes.byref(c), ctypes.byref(src),
+              int(layer0), int(q.shape[0]), int(q.shape[2]), int(top_k), qp, _kvq_ints(c, lens, "lens", q.device), op,
+              _ptr(sel))
+
+
+class LowramKvq:
+    """A quantised KV cache: its arrays (the caller's, or allocated here) and the workspace of
+    its attention calls, for up to ``max_q`` query tokens.  Not for two streams at the same time.
+
+    ``cfg``: the fields of ``lowram_kvq_config``; ``arrays``: k_code, k_scale, v_code, v_scale and
+    optionally k_mean and table (layouts of ``lowram.h``).  Without ``arrays`` they are allocated
+    on ``device``, with ``table`` as given (or none: sequence b owns pages b * max_pages + i)."""
+
+    def __init__(self, cfg, arrays=None, max_q: int = 1, table=None, device="cuda"):
+        import torch
+        self.config = c = LowramKvqConfigC.from_buffer_copy(kvq_config_struct(cfg))
+        self.max_q = int(max_q)
+        ws = lowram_kvq_workspace_bytes(c, c.n_layers, self.max_q)   # checks the config too
+        if arrays is None:
+            arrays = {n: torch.zeros(shape, dtype=dtype, device=device)
+                      for n, (shape, dtype) in _kvq_layouts(c).items() if n not in ("table", "err")}
+            arrays["table"] = table
+        get = lambda n: arrays.get(n) if isinstance(arrays, dict) else getattr(arrays, n, None)  # noqa: E731
+        self.arrays = {n: get(n) for n in _kvq_layouts(c)}
+        self._cache = _kvq_cache_struct(c, self.arrays)
+        self.device = dev = self.arrays["k_code"].device
+        if self.arrays["err"] is None:
+            self.arrays["err"] = torch.zeros(1, dtype=torch.int32, device=dev)
+            self._cache.err = self.arrays["err"].data_ptr()
+        self._workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
+        torch.cuda.current_stream(dev).synchronize()   # ready for whichever stream comes first
+
+    def _mine(self, t) -> None:
+        if t.device != self.device:
+            raise ValueError("the tensors of a call must be on the cache's device")
+
+    def write(self, k, v, pos, count=None, layer0: int = 0, stream=None) -> None:
+        """Quantise k, v [n_layers][B][n][Hkv][d] into slots pos[b] .. pos[b] + count[b] - 1."""
+        self._mine(k)
+        lowram_kvq_write(self.config, self._cache, layer0, k, v, pos, count, stream)
+
+    def read(self, pos, count=None, n: Optional[int] = None, layer0: int = 0, n_layers: Optional[int] = None, out=None,
+             stream=None):
+        """(k, v) [n_layers][B][n][Hkv][d] of tokens pos[b] + i; rows behind count[b] are left as
+        they are in ``out`` (zero without it)."""
+        import torch
+        if out is None:
+            c = self.config
+            shape = (c.n_layers - layer0 if n_layers is None else n_layers, c.batch, n, c.n_kv_heads, c.head_dim)
+            out = tuple(torch.zeros(shape, dtype=_kvq_dtype(c), device=self.device) for _ in range(2))
+        self._mine(out[0])
+        lowram_kvq_read(self.config, self._cache, layer0, out[0], out[1], pos, count, stream)
+        return out
+
+    def decode(self, q, lens, out=None, layer0: int = 0, stream=None):
+        """Attention of q [n_layers][B][n_q][Hq][d] over whole sequences of lens[b] tokens."""
+        import torch
+        self._mine(q)
+        if out is None:
+            out = torch.empty_like(q)
+        lowram_kvq_decode_attn(self.config, self._cache, layer0, q, lens, out, self._workspace, stream)
+        return out
+
+    def decode_sparse(self, q, lens, top_k: int, out=None, sel: bool = False, layer0: int = 0, stream=None):
+        """The same over each query's newest page and its top_k - 1 best older pages."""
+        import torch
+        self._mine(q)
+        if out is None:
+            out = torch.empty_like(q)
+        s = torch.empty(tuple(q.shape[:3]) + (self.config.n_kv_heads, int(top_k)), dtype=torch.int32,
+                        device=q.device) if sel else None
+        lowram_kvq_sparse_attn(self.config, self._cache, layer0, top_k, q, lens, out, s, stream)
+        return (out, s) if sel else out
+
+    def validate(self) -> int:
+        """The error word (bit 0: bad page id, bit 1: bad length, position or count), then cleared.
+        Synchronises."""
+        err = int(self.arrays["err"].item())
+        if err:
+            self.arrays["err"].zero_()
+        return err
+
+    def bytes(self) -> int:
+        """Bytes of the pool's codes, scales and page means."""
+        return sum(t.numel() * t.element_size() for n, t in self.arrays.items()
+                   if t is not None and n not in ("table", "err"))

@@ -1,0 +1,478 @@
+// The attention tile of the quantised KV cache: one warp, 16 tokens at a time, up to 8 NT query
+// rows (query heads of one KV head, and query tokens) against all of them.
+//
+// Both products run on mma.sync m16n8k16 (fp16 in, fp32 out) with the CODES as the A operand
+// (16 tokens, or 16 channels, a tile) and the queries as the 8 columns of B, so that few query
+// rows waste little of a tile.  A code needs no conversion: its bits, masked in place in a
+// 16-bit lane, ARE an fp16 number -- code n in the low mantissa bits is the subnormal n 2^-24, four
+// bits higher n 2^-20 -- and products with subnormals are exact.  Unpacking is one mask per two
+// codes and one shift per four; a 4-bit cache streams from HBM at the rate at which the warps
+// unpack it (about 1.6 thread instructions a code at d = 128), which is why the matrix
+// instruction that takes A from registers is used: tcgen05 reads A from shared memory, where
+// every code would first have to be stored as 16 bits.
+//
+// Scores.  x_t = sum_g s_tg (n_tg . q_g) + lo_tg sum(q_g): the scale and the offset of a group enter
+// per accumulator, in fp32, so keys are never rounded.  q is multiplied by a power of two per
+// row so that its largest entry lies in [2^13, 2^14): bf16 values stay exact in fp16 down to
+// 2^-27 of the largest (an fp32 q is split into two fp16 parts).
+//
+// Values.  o_c = sum_t (p_t s_tg) (n_tc - mid) + sum_t p_t (lo_tg + mid s_tg): w = p s 2^-E (times a constant) is rounded to fp16 once (fp32
+// calls: split in two parts), E following the value scales so that w stays within fp16's
+// normal range; the offsets are summed in fp32 beside.  A step's products are summed on their own
+// and added to the output in fp32 (the tensor core's sums are cut off, not rounded).  p = 2^(x - m) with a running m that moves
+// only when a score passes it by some factor -- w then still fits -- so most tiles neither reduce a
+// maximum across lanes nor rescale.
+//
+// Lane l holds r = l / 4, q = l % 4:
+//   A of the scores:  tokens r, r + 8; the cells 2q, 2q + 1 of every group -- one contiguous piece
+//                     of the row, whose order of groups inside cells is made for this load;
+//   scores C:         tokens r, r + 8 x columns 2q, 2q + 1;
+//   B of the values:  C's 8 x 8 halves transposed by movmatrix;
+//   A of the values:  cell r of tokens 2q, 2q + 1, 2q + 8, 2q + 9 (two tokens' words are merged, then
+//                     masked); code pair (2j, 2j + 1) gives rows r, r + 8 of product j;
+//   outputs C:        channels 64 g + 8 r + 2j (+ 1) x columns 2q, 2q + 1.
+#pragma once
+
+#include "kvq.cuh"
+
+namespace lowram {
+namespace kvq {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x = hi + lo with both in fp16 (lo holds the next 11 bits)
+__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_h2(a - __low2float(h), b - __high2float(h));
+}
+template <int BYTES> __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], const uint8_t* p) {
+  if constexpr (BYTES == 4) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (BYTES == 8) {
+    const uint2 t = *reinterpret_cast<const uint2*>(p);
+    w[0] = t.x;
+    w[1] = t.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = t.x;
+      w[4 * i + 1] = t.y;
+      w[4 * i + 2] = t.z;
+      w[4 * i + 3] = t.w;
+    }
+  }
+}
+
+// The two 16-bit lanes of half j (0, 1) of a cell: even codes in `a`, odd ones in `b` (4 bits: 16
+// times too large, made up for in B or in the output).
+template <int BITS>
+__device__ __forceinline__ void half_cell(const uint32_t* w, int j, uint32_t& a, uint32_t& b) {
+  if constexpr (BITS == 4) {
+    const uint32_t x = j ? w[0] >> 8 : w[0];
+    a = x & 0x000F000Fu;
+    b = x & 0x00F000F0u;
+  } else {
+    a = w[j] & 0x00FF00FFu;
+    b = (w[j] >> 8) & 0x00FF00FFu;
+  }
+}
+// Codes 2j, 2j + 1 of a cell of two tokens (low lanes: the first token).
+template <int BITS>
+__device__ __forceinline__ void pair_cell(const uint32_t* w0, const uint32_t* w1, int j, uint32_t& a, uint32_t& b) {
+  if constexpr (BITS == 4) {
+    uint32_t x = __byte_perm(w0[0], w1[0], j < 2 ? 0x5410 : 0x7632);
+    if (j & 1) x >>= 8;
+    a = x & 0x000F000Fu;
+    b = x & 0x00F000F0u;
+  } else {
+    const uint32_t x = __byte_perm(w0[j / 2], w1[j / 2], j & 1 ? 0x7632 : 0x5410);
+    a = x & 0x00FF00FFu;
+    b = (x >> 8) & 0x00FF00FFu;
+  }
+}
+
+template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
+  static constexpr int BITS = BITS_, D = D_, NT = NT_;
+  static constexpr bool F32 = F32_;
+  static constexpr int G = D / kGroup, ROW = D * BITS / 8, ROWS = 8 * NT;
+  static constexpr int SP = F32 ? 2 : 1;              // fp16 parts of q and of w
+  static constexpr int STEPS = 4 * G;                 // products of a score tile
+  static constexpr int BLOCK = 2 * 16 * ROW + 2 * 16 * G * 4;   // bytes of 16 tokens in shared memory
+  static constexpr int QFRAG = STEPS * NT * SP * 32 * 8;        // bytes of the queries' B operands
+  static constexpr int QMETA = ROWS * (1 + G) * 4;              // f'' and the group sums
+  static constexpr bool QREG = STEPS * NT * SP * 2 <= 32;       // B operands kept in registers
+  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  // A score may pass the running maximum by a factor of 2^kSlack in its weight, a value scale leave
+  // [2^E, 2^(E+1)) by a factor of kWide either way: w <= 2^(kSlack + 1) kWide kBias < 2^16, and what
+  // fp16's smallest step (2^-24) loses is 2^-30 (fp32: 2^-34) of a weight of one.
+  static constexpr float kSlack = F32 ? 2.f : 4.f, kWide = F32 ? 8.f : 16.f, kBias = F32 ? 1024.f : 64.f;
+
+  // Codes are summed as n - kMid, so that an average over many tokens is not a small difference of
+  // two large sums; the offsets become lo + kMid s.  kMidLow, kMidHigh: -kMid as two fp16 lanes, in
+  // the units of the codes of rows r and r + 8.
+  static constexpr float kMid = BITS == 4 ? 8.f : 128.f;
+  static constexpr uint32_t kMidLow = BITS == 4 ? 0x80088008u : 0x80808080u, kMidHigh = 0x80808080u;
+
+  float o[NT][G][4][4], ls[NT][G][2], l[NT][2], qs[NT][G][2];
+  float f[NT][2], mneg[NT][2], thr[NT][2];
+  float unit_inv;                                     // kBias 2^-E, 0 before the first scale
+  uint2 qr[QREG ? STEPS * NT * SP : 1];
+
+  // ---------------------------------------------------------------- queries
+  // Row j of the tile is query j (of `rows`; the others are zeros).  One warp fills row after row
+  // of the operands: q_row(j) gives its address.  meta: [ROWS] f'', then [ROWS][G] sums.
+  template <class QRow>
+  static __device__ __forceinline__ void prepare(uint8_t* frag, float* meta, int rows, int warp, int nwarps, QRow q_row) {
+    const int lane = threadIdx.x & 31;
+    constexpr int PER = D / 32;   // channels of a lane, consecutive: 2, 4 or 8 (within a cell)
+    for (int j = warp; j < ROWS; j += nwarps) {
+      float x[PER], mx = 0.f, sum = 0.f;
+      const T* src = q_row(j);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        x[i] = j < rows ? to_f<T>(src[lane * PER + i]) : 0.f;
+        mx = fmaxf(mx, fabsf(x[i]));
+        sum += x[i];
+      }
+      mx = warp_max(mx);
+      // a power of two: 2^13 <= mx sigma < 2^14 (1 for a row of zeros, or with an infinity)
+      const int e = (int)(__float_as_uint(mx) >> 23) - 127;
+      float sigma = 1.f;
+      if (e > -127 && e < 128) sigma = ldexpf(1.f, min(13 - e, 100));
+#pragma unroll
+      for (int o = 16 / G; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);   // 32 / G lanes hold a group
+      if (lane == 0) meta[j] = kLog2e * rsqrtf((float)D) * (16777216.f / sigma);
+      if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * sigma * (1.f / 16777216.f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = lane * PER + i, g = c / 64, w = c % 64 / 8, code = c % 8;
+        const int half = BITS == 4 ? code % 4 / 2 : code / 4, hi = BITS == 4 ? code / 4 : code % 4 / 2, reg = code % 2;
+        float y = x[i] * sigma;
+        if (BITS == 4 && reg) y *= 0.0625f;
+        const int step = (g * 2 + w % 2) * 2 + half;
+        __half* at = reinterpret_cast<__half*>(frag) + ((((step * NT + j / 8) * SP) * 32 + j % 8 * 4 + w / 2) * 2 + reg) * 2 + hi;
+        const __half h = __float2half_rn(y);
+        at[0] = h;
+        if constexpr (F32) at[32 * 4] = __float2half_rn(y - __half2float(h));
+      }
+    }
+  }
+  __device__ __forceinline__ void begin(const uint8_t* frag, const float* meta) {
+    const int lane = threadIdx.x & 31, q = lane & 3;
+    if constexpr (QREG) {
+#pragma unroll
+      for (int i = 0; i < STEPS * NT * SP; ++i) qr[i] = reinterpret_cast<const uint2*>(frag)[i * 32 + lane];
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int j = t * 8 + 2 * q + c;
+        f[t][c] = meta[j];
+        mneg[t][c] = 0.f;
+        thr[t][c] = -INFINITY;
+        l[t][c] = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          qs[t][g][c] = meta[ROWS + j * G + g];
+          ls[t][g][c] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[t][g][k][c] = o[t][g][k][2 + c] = 0.f;
+        }
+      }
+    unit_inv = 0.f;
+  }
+  __device__ __forceinline__ uint2 qop(const uint8_t* frag, int i) const {
+    if constexpr (QREG) return qr[i];
+    else return reinterpret_cast<const uint2*>(frag)[i * 32 + (threadIdx.x & 31)];
+  }
+
+  // ---------------------------------------------------------------- loading
+  // Starts the copies of 16 tokens whose first row (of slot 0 of their page on) is `row`.
+  static __device__ __forceinline__ void load(const Args& a, uint32_t dst, size_t row) {
+    const int lane = threadIdx.x & 31;
+    constexpr int CODE = 16 * ROW, META = 16 * G * 4;
+    const uint8_t* kc = a.k_code + row * ROW;
+    const uint8_t* vc = a.v_code + row * ROW;
+#pragma unroll
+    for (int i = 0; i < CODE / 512; ++i) {
+      cp16(dst + i * 512 + lane * 16, kc + i * 512 + lane * 16);
+      cp16(dst + CODE + i * 512 + lane * 16, vc + i * 512 + lane * 16);
+    }
+    constexpr int MP = META / 16;   // 16-byte pieces of the scales: 4, 8 or 16
+    if (lane < 2 * MP) {
+      const char* src = lane < MP ? reinterpret_cast<const char*>(a.k_scale + row * G) : reinterpret_cast<const char*>(a.v_scale + row * G);
+      cp16(dst + 2 * CODE + lane * 16, src + (lane % MP) * 16);
+    }
+  }
+
+  // ---------------------------------------------------------------- 16 TB tokens
+  // Token t of block i of this step has place tok + 16 i + t; column c of tile nt sees places below
+  // lim[nt][c].  EDGE: some place is masked (or block i is not there: bit i of `have` clear).
+  template <int TB, bool EDGE>
+  __device__ __forceinline__ void step(const uint8_t* slot, const uint8_t* frag, int tok, const int (&lim)[NT][2], unsigned have) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+    constexpr int CODE = 16 * ROW, META = 16 * G * 4;
+    float x[TB][NT][4];
+    // scores, in units of 1 / f''
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      const uint8_t* base = slot + b * BLOCK;
+      uint32_t k0[2 * G * BITS / 4], k1[2 * G * BITS / 4];
+      lds<2 * G * BITS>(k0, base + r * ROW + q * 2 * G * BITS);
+      lds<2 * G * BITS>(k1, base + (r + 8) * ROW + q * 2 * G * BITS);
+      uint32_t m0[G], m1[G];
+      lds<4 * G>(m0, base + 2 * CODE + r * 4 * G);
+      lds<4 * G>(m1, base + 2 * CODE + (r + 8) * 4 * G);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[b][t][k] = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float acc[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[t][k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a0, a1, a2, a3;
+            half_cell<BITS>(k0 + (e * G + g) * (BITS / 4), h, a0, a2);
+            half_cell<BITS>(k1 + (e * G + g) * (BITS / 4), h, a1, a3);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int s = 0; s < SP; ++s) mma_f16(acc[t], a0, a1, a2, a3, qop(frag, (((g * 2 + e) * 2 + h) * NT + t) * SP + s));
+          }
+        const float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&m0[g]));
+        const float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&m1[g]));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 u = k < 2 ? u0 : u1;
+            x[b][t][k] = fmaf(u.x, acc[t][k], fmaf(u.y, qs[t][g][k & 1], x[b][t][k]));
+          }
+      }
+      if constexpr (EDGE) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!(have >> b & 1) || tok + 16 * b + r + (k < 2 ? 0 : 8) >= lim[t][k & 1]) x[b][t][k] = -INFINITY;
+      }
+    }
+    // value scales and offsets of the tokens r, r + 8
+    float2 vs[TB][2][G];
+    bool high = false, there = false;
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t m[G];
+        lds<4 * G>(m, slot + b * BLOCK + 2 * CODE + META + (r + 8 * i) * 4 * G);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          vs[b][i][g] = __half22float2(*reinterpret_cast<const __half2*>(&m[g]));
+          if constexpr (EDGE) {
+            int most = lim[0][0];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) most = max(most, max(lim[t][0], lim[t][1]));
+            if (!(have >> b & 1) || tok + 16 * b + r + 8 * i >= most) vs[b][i][g] = make_float2(0.f, 0.f);
+          }
+          const float u = vs[b][i][g].x * unit_inv;
+          high |= u > 2.f * kWide * kBias;
+          there |= u > kBias / kWide;
+        }
+      }
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) high |= x[b][t][k] > thr[t][k & 1];
+    if (__any_sync(kFull, high) || !__any_sync(kFull, there)) move<TB>(x, vs);
+    // weights: p in x's place, the offsets' part, the sum of the weights
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = ex2(fmaf(x[b][t][k], f[t][k & 1], mneg[t][k & 1]));
+          x[b][t][k] = p;
+          l[t][k & 1] += p;
+        }
+    constexpr int CW = BITS / 4;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      uint2 w[TB][NT][SP];
+      float base[NT][4];   // -kMid sum_t w_t in every row: the products below then add w (n - kMid)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) base[t][k] = 0.f;
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          float y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 u = vs[b][k / 2][g];
+            const float p = x[b][t][k];
+            y[k] = p * (u.x * unit_inv);
+            float z = p * fmaf(kMid, u.x, u.y);
+            if constexpr (EDGE) {   // a place this column does not see may hold anything
+              const bool seen = (have >> b & 1) && tok + 16 * b + r + (k < 2 ? 0 : 8) < lim[t][k & 1];
+              y[k] = seen ? y[k] : 0.f;
+              z = seen ? z : 0.f;
+            }
+            ls[t][g][k & 1] += z;
+          }
+          if constexpr (F32) {
+            uint32_t h0, h1, l0, l1;
+            split_h2(y[0], y[1], h0, l0);
+            split_h2(y[2], y[3], h1, l1);
+            w[b][t][0] = make_uint2(trans8x8(h0), trans8x8(h1));
+            w[b][t][SP - 1] = make_uint2(trans8x8(l0), trans8x8(l1));
+          } else {
+            w[b][t][0] = make_uint2(trans8x8(pack_h2(y[0], y[1])), trans8x8(pack_h2(y[2], y[3])));
+          }
+#pragma unroll
+          for (int i = SP - 1; i >= 0; --i) mma_f16(base[t], kMidLow, kMidHigh, kMidLow, kMidHigh, w[b][t][i]);
+        }
+      }
+      uint32_t v[TB][4][CW];
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          lds<4 * CW>(v[b][i], slot + b * BLOCK + CODE + (2 * q + (i & 1) + (i >> 1) * 8) * ROW + (r * G + g) * BITS);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float acc[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[t][k] = base[t][k];
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          uint32_t a0, a1, a2, a3;
+          pair_cell<BITS>(v[b][0], v[b][1], j, a0, a1);
+          pair_cell<BITS>(v[b][2], v[b][3], j, a2, a3);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = SP - 1; i >= 0; --i) mma_f16(acc[t], a0, a1, a2, a3, w[b][t][i]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[t][g][j][k] += acc[t][k];
+      }
+    }
+  }
+
+  // A score passed the running maximum, or the value scales left their unit: both anew.
+  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][4], const float2 (&vs)[TB][2][G]) {
+    float s = 0.f;
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g) s = fmaxf(s, vs[b][i][g].x);
+    s = warp_max(s);
+    float inv = unit_inv, scale = 1.f;
+    if (s > 0.f && s < INFINITY && (unit_inv == 0.f || s * unit_inv > 2.f * kWide * kBias || !(s * unit_inv > kBias / kWide))) {
+      inv = kBias * __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);   // kBias <= s inv < 2 kBias
+      scale = unit_inv == 0.f ? 1.f : inv / unit_inv;
+      unit_inv = inv;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < TB; ++b) mx = fmaxf(mx, fmaxf(x[b][t][c], x[b][t][2 + c]));
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, i));
+        float alpha = 1.f;
+        if (mx > thr[t][c]) {
+          const float m = -mx * f[t][c];
+          alpha = thr[t][c] == -INFINITY ? 0.f : ex2(m - mneg[t][c]);
+          mneg[t][c] = m;
+          thr[t][c] = mx + kSlack / f[t][c];
+          l[t][c] *= alpha;
+        }
+        const float both = alpha * scale;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          ls[t][g][c] *= alpha;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[t][g][j][c] *= both;
+            o[t][g][j][2 + c] *= both;
+          }
+        }
+      }
+  }
+
+  // ---------------------------------------------------------------- end
+  // Running maximum of column (t, c) in log2 units, -inf without a token.
+  __device__ __forceinline__ float top(int t, int c) const { return thr[t][c] == -INFINITY ? -INFINITY : -mneg[t][c]; }
+  // Adds up what lanes hold apart: sums of the weights and of the offsets' part.
+  __device__ __forceinline__ void reduce() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) {
+          l[t][c] += __shfl_xor_sync(kFull, l[t][c], i);
+#pragma unroll
+          for (int g = 0; g < G; ++g) ls[t][g][c] += __shfl_xor_sync(kFull, ls[t][g][c], i);
+        }
+  }
+  // Output of channel 64 g + 8 r + 2 j + i, column c (unnormalised), after reduce().
+  __device__ __forceinline__ float value(int t, int g, int j, int i, int c) const {
+    const float un = unit_inv == 0.f ? 0.f : (i && BITS == 4 ? 1048576.f : 16777216.f) / unit_inv;
+    return fmaf(o[t][g][j][2 * i + c], un, ls[t][g][c]);
+  }
+};
+
+}  // namespace kvq
+}  // namespace lowram

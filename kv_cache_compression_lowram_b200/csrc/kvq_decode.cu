@@ -1,46 +1,341 @@
 // Quantised KV cache: attention of the last tokens over whole sequences.
 //
-// Simple form: one CTA per (layer, sequence, query token, query head), one pass over the
-// tokens with the running maximum and sum of the softmax.
+// Bound by HBM: 2 (d bits / 8 + d / 16) bytes per cached token and KV head, read once per 8 or 16
+// query rows.  All steps of all units -- a unit is (sequence, layer, KV head, tile of query rows), a
+// step 16 or 32 of its tokens -- form one line that is cut into equal pieces, one per CTA, so
+// ragged lengths and few long sequences load the SMs evenly without the host knowing a length.
+// A CTA's four warps take its steps in turn, each through a ring of its own in shared memory that
+// cp.async fills ahead, across unit borders; at the end of a unit's part they join their sums.
+// A unit that several CTAs share is joined by the one that finishes last, in the order of the
+// pieces (the result does not depend on which that is).
 #include "kvq.cuh"
-#include "kvq_simple.cuh"
+#include "kvq_attend.cuh"
 
 namespace lowram {
 namespace kvq {
 namespace {
 
-template <typename T, int BITS, int D>
-__global__ void __launch_bounds__(kSimpleThreads) decode_kernel(Args a, const T* __restrict__ q, const int32_t* __restrict__ lens,
-                                                                T* __restrict__ out) {
-  const unsigned x = blockIdx.x;   // ((layer * B + b) * n + i) * Hq + j
-  const int j = x % a.Hq, i = x / a.Hq % a.n, b = x / a.Hq / a.n % a.B, layer = x / a.Hq / a.n / a.B;
-  if (threadIdx.x == 0 && i == 0 && j == 0 && len_bad(a, lens, b)) flag(a, KVQ_ERR_RANGE);
-  const int lim = len_of(a, lens, b) - a.n + 1 + i;
-  SimpleAttend<T, BITS, D> s;
-  s.begin(q + (size_t)x * D);
-  for (int pg = 0; (pg << a.page_log2) < lim; ++pg)
-    s.page(a, a.layer0 + layer, b, j / a.g, pg, min(a.page, lim - (pg << a.page_log2)));
-  s.end(out + (size_t)x * D);
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxWorkers = 640;
+constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are less
+
+template <int BITS, int D, int NT, bool F32> struct Plan {
+  using Tl = Tile<BITS, D, NT, F32>;
+  static constexpr int TB = Tl::BLOCK <= 2304 ? 2 : 1;      // 16-token blocks of a step
+  static constexpr int SLOT = TB * Tl::BLOCK;
+  static constexpr int STAGES = SLOT > 4608 ? 2 : 3;
+  static constexpr int JOIN = kWarps * Tl::ROWS * D * 4;    // the warps' sums
+  static constexpr int RING = kWarps * STAGES * SLOT;
+  static constexpr int SMEM = RING + JOIN + Tl::QFRAG + Tl::QMETA + kWarps * Tl::ROWS * 8 + 16;
+  static constexpr int MINB = SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);
+};
+
+struct Walk {   // a place on the line of steps
+  int b, u, st, n;   // sequence, unit inside it, step inside the unit, steps of its units
+};
+
+template <class P> struct Line {
+  const Args& a;
+  const int32_t* lens;
+  int U;   // units of a sequence
+  static constexpr int TOK = 16 * P::TB;
+  __device__ __forceinline__ int steps(int b) const { return max(1, (len_of(a, lens, b) + TOK - 1) / TOK); }
+  __device__ long long total() const {   // the same on every lane
+    const int lane = threadIdx.x & 31;
+    long long t = 0;
+    for (int b = lane; b < a.B; b += 32) t += steps(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+    return t * U;
+  }
+  __device__ Walk at(long long x) const {   // 0 <= x < total
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int b = b0 + lane, n = b < a.B ? steps(b) : 0;
+      long long inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned past = __ballot_sync(kFull, (before + inc) * U > x);
+      if (past) {
+        const int w = __ffs(past) - 1;
+        const long long start = (before + __shfl_sync(kFull, inc - n, w)) * U;
+        const int nn = __shfl_sync(kFull, n, w), rel = (int)((x - start) / nn);
+        return Walk{b0 + w, rel, (int)(x - start - (long long)rel * nn), nn};
+      }
+      before += __shfl_sync(kFull, inc, 31);
+    }
+  }
+  __device__ __forceinline__ void next_unit(Walk& w) const {
+    w.st = 0;
+    if (++w.u == U) {
+      w.u = 0;
+      if (++w.b < a.B) w.n = steps(w.b);
+    }
+  }
+  __device__ __forceinline__ void forward(Walk& w, int k) const {
+    w.st += k;
+    while (w.b < a.B && w.st >= w.n) {
+      const int rest = w.st - w.n;
+      next_unit(w);
+      w.st = rest;
+    }
+  }
+};
+
+template <int BITS, int D, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT, F32>::MINB)
+decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
+              unsigned* __restrict__ arrived, float* __restrict__ part) {
+  using P = Plan<BITS, D, NT, F32>;
+  using Tl = typename P::Tl;
+  using T = typename Tl::T;
+  constexpr int ROWS = Tl::ROWS, G = Tl::G, TB = P::TB;
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint8_t* frag = sm + P::RING;
+  float* join = reinterpret_cast<float*>(frag + Tl::QFRAG);
+  float* meta = join + P::JOIN / 4;
+  float* tops = meta + Tl::QMETA / 4;          // [warp][row] running maxima, then the sums of the weights
+  int* shared_int = reinterpret_cast<int*>(tops + 2 * kWarps * ROWS);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const T* q = static_cast<const T*>(qv);
+  T* out = static_cast<T*>(outv);
+  const int rows_all = a.n * a.g;
+  const Line<P> line{a, lens, a.n_layers * a.Hkv * row_tiles};
+  const long long total = line.total();
+  // at least one step per warp where there are few
+  const long long want = (total + kWarps - 1) / kWarps;
+  const int workers = want < gridDim.x ? (int)want : gridDim.x, me = blockIdx.x;
+  if (me >= workers) return;
+  if (me == 0)
+    for (int b = tid; b < a.B; b += kThreads)
+      if (len_bad(a, lens, b)) flag(a, KVQ_ERR_RANGE);
+  const long long s0 = tile_begin(total, workers, me), s1 = tile_begin(total, workers, me + 1);
+  Walk cur = line.at(s0), ahead = cur;
+  line.forward(ahead, warp);
+  long long xa = s0 + warp;                     // the next step to load
+  uint8_t* ring = sm + warp * P::STAGES * P::SLOT;
+  const uint32_t ring_u = smem_u32(ring);
+  unsigned have = 0;                            // TB bits per step in flight: blocks that are there
+  int pending = 0, in = 0, rd = 0;
+  auto issue = [&]() {
+    if (xa < s1) {
+      const int h = ahead.u / row_tiles % a.Hkv, layer = ahead.u / row_tiles / a.Hkv, len = len_of(a, lens, ahead.b);
+#pragma unroll
+      for (int i = 0; i < TB; ++i) {
+        const int tok = (ahead.st * TB + i) * 16;
+        if (tok < len) {
+          const int pid = page_of(a, ahead.b, tok >> a.page_log2);
+          if (pid >= 0) {
+            Tl::load(a, ring_u + in * P::SLOT + i * Tl::BLOCK,
+                     row0_of(a, a.layer0 + layer, pid, h) + (tok & (a.page - 1)));
+            have |= 1u << (pending * TB + i);
+          } else if (lane == 0) {
+            flag(a, KVQ_ERR_PAGE);
+          }
+        }
+      }
+      ++pending;
+      in = in + 1 == P::STAGES ? 0 : in + 1;
+      xa += kWarps;
+      line.forward(ahead, kWarps);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < P::STAGES - 1; ++i) issue();
+
+  Tl tile;
+  for (long long x = s0; x < s1;) {             // a unit's part at a time
+    const long long x1 = min(s1, x + (cur.n - cur.st)), unit0 = x - cur.st;
+    const int rt = cur.u % row_tiles, h = cur.u / row_tiles % a.Hkv, layer = cur.u / row_tiles / a.Hkv;
+    const int row_base = rt * ROWS, rows = min(ROWS, rows_all - row_base), len = len_of(a, lens, cur.b);
+    // row j of the tile: query token (row_base + j) / g, head (row_base + j) % g of the KV head
+    const size_t qbase = ((size_t)layer * a.B + cur.b) * a.n;
+    auto row_at = [&](int j) {
+      const int i = (row_base + j) / a.g, jj = (row_base + j) % a.g;
+      return ((qbase + i) * a.Hq + (size_t)h * a.g + jj) * D;
+    };
+    Tl::prepare(frag, meta, rows, warp, kWarps, [&](int j) { return q + (j < rows ? row_at(j) : 0); });
+    __syncthreads();
+    tile.begin(frag, meta);
+    int lim[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int j = min(t * 8 + 2 * (lane & 3) + c, rows - 1);
+        lim[t][c] = len - a.n + 1 + (row_base + j) / a.g;
+      }
+    const int least = len - a.n + 1 + row_base / a.g;
+    // this warp's steps of the part: x = s0 + warp modulo kWarps
+    int st = cur.st + (int)((warp - (x - s0) % kWarps + kWarps) % kWarps);
+    const int st1 = cur.st + (int)(x1 - x);
+    for (; st < st1; st += kWarps) {
+      cp_wait<P::STAGES - 2>();
+      __syncwarp();
+      const unsigned there = have & ((1u << TB) - 1);
+      have >>= TB;
+      --pending;
+      const uint8_t* slot = ring + rd * P::SLOT;
+      const int tok = st * Line<P>::TOK;
+      if (there == (1u << TB) - 1 && tok + Line<P>::TOK <= least) tile.template step<TB, false>(slot, frag, tok, lim, there);
+      else tile.template step<TB, true>(slot, frag, tok, lim, there);
+      rd = rd + 1 == P::STAGES ? 0 : rd + 1;
+      __syncwarp();
+      issue();
+    }
+    // join the warps: common maximum, scaled sums, channels added warp by warp
+    tile.reduce();
+    if (lane < 4) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int j = t * 8 + 2 * lane + c;
+          tops[warp * ROWS + j] = tile.top(t, c);
+          tops[(kWarps + warp) * ROWS + j] = tile.l[t][c];
+        }
+    }
+    __syncthreads();
+    {
+      const int r = lane >> 2, qd = lane & 3;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int j = t * 8 + 2 * qd + c;
+          float m = tops[j];
+#pragma unroll
+          for (int w = 1; w < kWarps; ++w) m = fmaxf(m, tops[w * ROWS + j]);
+          const float mine = tops[warp * ROWS + j], fac = mine == -INFINITY ? 0.f : ex2(mine - m);
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float2 v = make_float2(tile.value(t, g, k, 0, c), tile.value(t, g, k, 1, c));
+              if (fac == 0.f) v = make_float2(0.f, 0.f);   // no token: its sums are zeros times anything
+              else { v.x *= fac; v.y *= fac; }
+              *reinterpret_cast<float2*>(join + (size_t)(warp * ROWS + j) * D + 64 * g + 8 * r + 2 * k) = v;
+            }
+        }
+    }
+    __syncthreads();
+    const bool whole = unit0 >= s0 && unit0 + cur.n <= s1;
+    const int c_first = whole ? me : cta_of_tile(total, workers, unit0), c_last = whole ? me : cta_of_tile(total, workers, unit0 + cur.n - 1);
+    constexpr int REC = D + 2;
+    float* rec = part + (size_t)(2 * me + (unit0 >= s0 ? 1 : 0)) * ROWS * REC;
+    for (int e = tid; e < rows * D; e += kThreads) {
+      const int j = e / D, c = e % D;
+      float m = tops[j], lsum = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, tops[w * ROWS + j]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = tops[w * ROWS + j];
+        if (mw != -INFINITY) lsum = fmaf(tops[(kWarps + w) * ROWS + j], ex2(mw - m), lsum);
+        v += join[(size_t)(w * ROWS + j) * D + c];
+      }
+      if (whole) {
+        out[row_at(j) + c] = from_f<T>(m == -INFINITY ? 0.f : v / lsum);
+      } else {
+        rec[j * REC + c] = v;
+        if (c == 0) {
+          rec[j * REC + D] = m;
+          rec[j * REC + D + 1] = lsum;
+        }
+      }
+    }
+    if (!whole) {
+      // the last CTA of the unit to come joins all parts, in their order
+      __threadfence();
+      __syncthreads();
+      unsigned* cnt = arrived + (size_t)cur.b * line.U + cur.u;
+      if (tid == 0) {
+        const int last = atomicAdd(cnt, 1u) == (unsigned)(c_last - c_first);
+        if (last) *cnt = 0;                     // ready for the next call
+        *shared_int = last;
+      }
+      __syncthreads();
+      if (*shared_int) {
+        __threadfence();
+        for (int e = tid; e < rows * D; e += kThreads) {
+          const int j = e / D, c = e % D;
+          float m = -INFINITY, lsum = 0.f, v = 0.f;
+          for (int w = c_first; w <= c_last; ++w) {
+            const float* p = part + ((size_t)(2 * w + (w == c_first ? 1 : 0)) * ROWS + j) * REC;
+            const float mw = __ldcg(p + D), lw = __ldcg(p + D + 1), vw = __ldcg(p + c);
+            if (mw == -INFINITY) continue;
+            const float mn = fmaxf(m, mw), fo = m == -INFINITY ? 0.f : ex2(m - mn), fn = ex2(mw - mn);
+            lsum = lsum * fo + lw * fn;
+            v = v * fo + vw * fn;
+            m = mn;
+          }
+          out[row_at(j) + c] = from_f<T>(m == -INFINITY ? 0.f : v / lsum);
+        }
+      }
+    }
+    __syncthreads();                            // the queries' operands and the sums may be written anew
+    x = x1;
+    cur.st += (int)(x1 - cur.st - unit0);
+    if (cur.st >= cur.n) line.next_unit(cur);
+  }
+  cp_wait<0>();
 }
 
-template <typename T, int BITS>
-cudaError_t go(const Args& a, const void* q, const int32_t* lens, void* out, cudaStream_t s) {
-  const unsigned grid = (unsigned)((long long)a.n_layers * a.B * a.n * a.Hq);
-  const T* qt = static_cast<const T*>(q);
-  T* ot = static_cast<T*>(out);
-  if (a.d == 64) decode_kernel<T, BITS, 64><<<grid, kSimpleThreads, 0, s>>>(a, qt, lens, ot);
-  else if (a.d == 128) decode_kernel<T, BITS, 128><<<grid, kSimpleThreads, 0, s>>>(a, qt, lens, ot);
-  else decode_kernel<T, BITS, 256><<<grid, kSimpleThreads, 0, s>>>(a, qt, lens, ot);
+// Query rows of a tile: 16 where there are more than 8 and the sums fit the registers (d <= 128).
+int rows_tile(const Args& a) { return a.d <= 128 && a.n * a.g > 8 ? 16 : 8; }
+
+template <int BITS, int D, int NT, bool F32>
+cudaError_t go(const Args& a, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s) {
+  using P = Plan<BITS, D, NT, F32>;
+  // per device: the kernel's attribute and the CTAs that are resident at once
+  static int workers[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int w = dev < 64 ? workers[dev] : 0;
+  if (!w) {
+    int sm = 0, per = 0;
+    if ((e = cudaFuncSetAttribute(decode_kernel<BITS, D, NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, decode_kernel<BITS, D, NT, F32>, kThreads, P::SMEM)) != cudaSuccess) return e;
+    w = sm * (per < 1 ? 1 : per);
+    if (w > kMaxWorkers) w = kMaxWorkers;
+    if (dev < 64) workers[dev] = w;
+  }
+  static_assert((size_t)2 * kMaxWorkers * 8 * NT * (D + 2) * 4 <= kPartBytes, "parts");
+  // the parts first: the counters of every kind of call start at one place and stay zero between calls
+  float* part = static_cast<float*>(ws);
+  unsigned* arrived = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kPartBytes);
+  const int tiles = (a.n * a.g + 8 * NT - 1) / (8 * NT);
+  decode_kernel<BITS, D, NT, F32><<<w, kThreads, P::SMEM, s>>>(a, tiles, q, lens, out, arrived, part);
   return cudaGetLastError();
+}
+
+template <int BITS, bool F32>
+cudaError_t by_shape(const Args& a, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s) {
+  const bool two = rows_tile(a) == 16;
+  if (a.d == 64) return two ? go<BITS, 64, 2, F32>(a, q, lens, out, ws, s) : go<BITS, 64, 1, F32>(a, q, lens, out, ws, s);
+  if (a.d == 128) return two ? go<BITS, 128, 2, F32>(a, q, lens, out, ws, s) : go<BITS, 128, 1, F32>(a, q, lens, out, ws, s);
+  return go<BITS, 256, 1, F32>(a, q, lens, out, ws, s);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(const Args&) { return 16; }
+size_t decode_workspace_bytes(const Args& a) {
+  const int rt = rows_tile(a), tiles = (a.n * a.g + rt - 1) / rt;
+  return kPartBytes + (size_t)a.B * a.n_layers * a.Hkv * tiles * 4;
+}
 
-cudaError_t launch_decode(const Args& a, int dtype, const void* q, const int32_t* lens, void* out, void*, cudaStream_t s) {
-  if (dtype == LOWRAM_F32) return a.bits == 4 ? go<float, 4>(a, q, lens, out, s) : go<float, 8>(a, q, lens, out, s);
-  return a.bits == 4 ? go<__nv_bfloat16, 4>(a, q, lens, out, s) : go<__nv_bfloat16, 8>(a, q, lens, out, s);
+cudaError_t launch_decode(const Args& a, int dtype, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s) {
+  if (dtype == LOWRAM_F32)
+    return a.bits == 4 ? by_shape<4, true>(a, q, lens, out, ws, s) : by_shape<8, true>(a, q, lens, out, ws, s);
+  return a.bits == 4 ? by_shape<4, false>(a, q, lens, out, ws, s) : by_shape<8, false>(a, q, lens, out, ws, s);
 }
 
 }  // namespace kvq

@@ -146,6 +146,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
   float o[NT][G][4][4], ls[NT][G][2], l[NT][2], qs[NT][G][2];
   float f[NT][2], mneg[NT][2], thr[NT][2];
   float unit_inv;                                     // kBias 2^-E, 0 before the first scale
+  uint32_t top_s;                                     // the largest scale that needs no new unit (fp16 bits)
   uint2 qr[QREG ? STEPS * NT * SP : 1];
 
   // ---------------------------------------------------------------- queries
@@ -211,6 +212,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
         }
       }
     unit_inv = 0.f;
+    top_s = 0;
   }
   __device__ __forceinline__ uint2 qop(const uint8_t* frag, int i) const {
     if constexpr (QREG) return qr[i];
@@ -218,21 +220,20 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
   }
 
   // ---------------------------------------------------------------- loading
-  // Starts the copies of 16 tokens whose first row (of slot 0 of their page on) is `row`.
+  // Starts the copies of 16 tokens, the first at row `row` of the pool.
   static __device__ __forceinline__ void load(const Args& a, uint32_t dst, size_t row) {
     const int lane = threadIdx.x & 31;
     constexpr int CODE = 16 * ROW, META = 16 * G * 4;
-    const uint8_t* kc = a.k_code + row * ROW;
-    const uint8_t* vc = a.v_code + row * ROW;
+    const size_t at = row * ROW + lane * 16;
 #pragma unroll
     for (int i = 0; i < CODE / 512; ++i) {
-      cp16(dst + i * 512 + lane * 16, kc + i * 512 + lane * 16);
-      cp16(dst + CODE + i * 512 + lane * 16, vc + i * 512 + lane * 16);
+      cp16(dst + i * 512 + lane * 16, a.k_code + at + i * 512);
+      cp16(dst + CODE + i * 512 + lane * 16, a.v_code + at + i * 512);
     }
     constexpr int MP = META / 16;   // 16-byte pieces of the scales: 4, 8 or 16
     if (lane < 2 * MP) {
-      const char* src = lane < MP ? reinterpret_cast<const char*>(a.k_scale + row * G) : reinterpret_cast<const char*>(a.v_scale + row * G);
-      cp16(dst + 2 * CODE + lane * 16, src + (lane % MP) * 16);
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(lane < MP ? a.k_scale : a.v_scale);
+      cp16(dst + 2 * CODE + lane * 16, src + row * (G * 4) + (lane % MP) * 16);
     }
   }
 
@@ -296,35 +297,31 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
       }
     }
     // value scales and offsets of the tokens r, r + 8
-    float2 vs[TB][2][G];
-    bool high = false, there = false;
+    uint32_t vm[TB][2][G], most_s = 0;   // (s, lo) pairs; the largest s in the low half (s >= 0, so its bits are ordered)
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint32_t m[G];
-        lds<4 * G>(m, slot + b * BLOCK + 2 * CODE + META + (r + 8 * i) * 4 * G);
+        lds<4 * G>(vm[b][i], slot + b * BLOCK + 2 * CODE + META + (r + 8 * i) * 4 * G);
+        if constexpr (EDGE) {
+          int most = lim[0][0];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          vs[b][i][g] = __half22float2(*reinterpret_cast<const __half2*>(&m[g]));
-          if constexpr (EDGE) {
-            int most = lim[0][0];
+          for (int t = 0; t < NT; ++t) most = max(most, max(lim[t][0], lim[t][1]));
+          if (!(have >> b & 1) || tok + 16 * b + r + 8 * i >= most)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) most = max(most, max(lim[t][0], lim[t][1]));
-            if (!(have >> b & 1) || tok + 16 * b + r + 8 * i >= most) vs[b][i][g] = make_float2(0.f, 0.f);
-          }
-          const float u = vs[b][i][g].x * unit_inv;
-          high |= u > 2.f * kWide * kBias;
-          there |= u > kBias / kWide;
+            for (int g = 0; g < G; ++g) vm[b][i][g] = 0;
         }
+#pragma unroll
+        for (int g = 0; g < G; ++g) most_s = __vmaxu2(most_s, vm[b][i][g]);
       }
+    bool high = (most_s & 0xffffu) > top_s;
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) high |= x[b][t][k] > thr[t][k & 1];
-    if (__any_sync(kFull, high) || !__any_sync(kFull, there)) move<TB>(x, vs);
+    if (__any_sync(kFull, high)) move<TB>(x, most_s & 0xffffu);
     // weights: p in x's place, the offsets' part, the sum of the weights
 #pragma unroll
     for (int b = 0; b < TB; ++b)
@@ -337,23 +334,34 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
           l[t][k & 1] += p;
         }
     constexpr int CW = BITS / 4;
+    uint32_t v[TB][4][G * CW];   // cell r of the tokens 2q, 2q + 1, 2q + 8, 2q + 9
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds<G * BITS>(v[b][i], slot + b * BLOCK + CODE + (2 * q + (i & 1) + (i >> 1) * 8) * ROW + r * G * BITS);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       uint2 w[TB][NT][SP];
       float base[NT][4];   // -kMid sum_t w_t in every row: the products below then add w (n - kMid)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) base[t][k] = 0.f;
 #pragma unroll
-        for (int b = 0; b < TB; ++b) {
+      for (int b = 0; b < TB; ++b) {
+        float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][0][g]));
+        float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][1][g]));
+        u0 = make_float2(u0.x * unit_inv, fmaf(kMid, u0.x, u0.y));
+        u1 = make_float2(u1.x * unit_inv, fmaf(kMid, u1.x, u1.y));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
           float y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 u = vs[b][k / 2][g];
+            const float2 u = k < 2 ? u0 : u1;
             const float p = x[b][t][k];
-            y[k] = p * (u.x * unit_inv);
-            float z = p * fmaf(kMid, u.x, u.y);
+            y[k] = p * u.x;
+            float z = p * u.y;
             if constexpr (EDGE) {   // a place this column does not see may hold anything
               const bool seen = (have >> b & 1) && tok + 16 * b + r + (k < 2 ? 0 : 8) < lim[t][k & 1];
               y[k] = seen ? y[k] : 0.f;
@@ -374,12 +382,6 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
           for (int i = SP - 1; i >= 0; --i) mma_f16(base[t], kMidLow, kMidHigh, kMidLow, kMidHigh, w[b][t][i]);
         }
       }
-      uint32_t v[TB][4][CW];
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          lds<4 * CW>(v[b][i], slot + b * BLOCK + CODE + (2 * q + (i & 1) + (i >> 1) * 8) * ROW + (r * G + g) * BITS);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float acc[NT][4];
@@ -390,8 +392,8 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
           uint32_t a0, a1, a2, a3;
-          pair_cell<BITS>(v[b][0], v[b][1], j, a0, a1);
-          pair_cell<BITS>(v[b][2], v[b][3], j, a2, a3);
+          pair_cell<BITS>(v[b][0] + g * CW, v[b][1] + g * CW, j, a0, a1);
+          pair_cell<BITS>(v[b][2] + g * CW, v[b][3] + g * CW, j, a2, a3);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -405,21 +407,18 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
     }
   }
 
-  // A score passed the running maximum, or the value scales left their unit: both anew.
-  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][4], const float2 (&vs)[TB][2][G]) {
-    float s = 0.f;
-#pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int g = 0; g < G; ++g) s = fmaxf(s, vs[b][i][g].x);
-    s = warp_max(s);
-    float inv = unit_inv, scale = 1.f;
-    if (s > 0.f && s < INFINITY && (unit_inv == 0.f || s * unit_inv > 2.f * kWide * kBias || !(s * unit_inv > kBias / kWide))) {
-      inv = kBias * __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);   // kBias <= s inv < 2 kBias
+  // A score passed the running maximum, or a value scale its unit's room: both anew.  A unit that
+  // has become far too large is made smaller here as well: the scales it was made for have lost
+  // their weight only if the maximum has moved.
+  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][4], uint32_t most_s) {
+    const uint32_t sb = __reduce_max_sync(kFull, most_s);
+    const float s = __half2float(__ushort_as_half((unsigned short)sb));
+    float scale = 1.f;
+    if (sb && sb < 0x7c00u && (unit_inv == 0.f || sb > top_s || !(s * unit_inv > kBias / kWide))) {
+      const float inv = kBias * __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);   // kBias <= s inv < 2 kBias
       scale = unit_inv == 0.f ? 1.f : inv / unit_inv;
       unit_inv = inv;
+      top_s = __half_as_ushort(__float2half_rz(fminf(kWide * 2.f * kBias / inv, 65504.f)));   // a power of two
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)

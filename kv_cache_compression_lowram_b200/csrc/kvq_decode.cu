@@ -18,7 +18,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxWorkers = 640;
-constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are less
+constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are fewer
 
 template <int BITS, int D, int NT, bool F32> struct Plan {
   using Tl = Tile<BITS, D, NT, F32>;
@@ -87,6 +87,73 @@ template <class P> struct Line {
   }
 };
 
+// The parts of a unit (CTAs c_first .. c_last), joined in their order.  The weights of a chunk of
+// parts are computed side by side, then each thread sums four channels over them with its loads in
+// flight together.  wt: [kChunk][ROWS] floats; norm: [ROWS] maxima, then [ROWS] sums.
+template <class P, class Store>
+__device__ __forceinline__ void join_parts(const float* part, int c_first, int c_last, int rows, float* wt, float* norm, Store store) {
+  constexpr int ROWS = P::Tl::ROWS, D = P::Tl::D, REC = ROWS * (D + 2), kChunk = P::JOIN / 4 / ROWS;
+  static_assert(2 * ROWS <= kThreads, "rows");
+  const int tid = threadIdx.x, n = c_last - c_first + 1;
+  auto at = [&](int i) { return part + (size_t)(2 * (c_first + i) + (i == 0 ? 1 : 0)) * REC; };
+  // the maxima of all parts: kThreads / ROWS threads a row
+  constexpr int PER = kThreads / ROWS;
+  const int jr = tid % ROWS, pr = tid / ROWS;
+  float m = -INFINITY;
+  for (int i = pr; i < n; i += PER) m = fmaxf(m, __ldcg(at(i) + ROWS * D + jr));
+  __syncthreads();
+  wt[pr * ROWS + jr] = m;
+  __syncthreads();
+  if (tid < ROWS) {
+    for (int i = 1; i < PER; ++i) m = fmaxf(m, wt[i * ROWS + tid]);
+    norm[tid] = m;
+    norm[ROWS + tid] = 0.f;
+  }
+  constexpr int QUADS = ROWS * D / 4, MINE = (QUADS + kThreads - 1) / kThreads;
+  float4 v[MINE];
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += kChunk) {
+    const int nc = min(kChunk, n - i0);
+    __syncthreads();
+    for (int e = tid; e < nc * ROWS; e += kThreads) {
+      const float mj = norm[e % ROWS], mp = __ldcg(at(i0 + e / ROWS) + ROWS * D + e % ROWS);
+      wt[e] = mp == -INFINITY ? 0.f : ex2(mp - mj);
+    }
+    __syncthreads();
+    if (tid < ROWS) {
+      float l = norm[ROWS + tid];
+      for (int i = 0; i < nc; ++i) l = fmaf(wt[i * ROWS + tid], __ldcg(at(i0 + i) + ROWS * D + ROWS + tid), l);
+      norm[ROWS + tid] = l;
+    }
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      const int e = tid + k * kThreads, j = e / (D / 4);
+      if (j >= rows) continue;
+#pragma unroll 8
+      for (int i = 0; i < nc; ++i) {
+        const float4 p = __ldcg(reinterpret_cast<const float4*>(at(i0 + i)) + e);
+        const float w = wt[i * ROWS + j];
+        if (w != 0.f) {
+          v[k].x = fmaf(w, p.x, v[k].x);
+          v[k].y = fmaf(w, p.y, v[k].y);
+          v[k].z = fmaf(w, p.z, v[k].z);
+          v[k].w = fmaf(w, p.w, v[k].w);
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    const int e = tid + k * kThreads, j = e / (D / 4);
+    if (j >= rows) continue;
+    const float inv = norm[j] == -INFINITY ? 0.f : 1.f / norm[ROWS + j];
+    store(j, e % (D / 4) * 4, norm[j] == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                  : make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv));
+  }
+}
+
 template <int BITS, int D, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT, F32>::MINB)
 decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
@@ -122,20 +189,32 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   const uint32_t ring_u = smem_u32(ring);
   unsigned have = 0;                            // TB bits per step in flight: blocks that are there
   int pending = 0, in = 0, rd = 0;
+  // what the loads of a unit need, made anew when `ahead` enters another one
+  int seen_b = -1, seen_u = -1, len_a = 0;
+  size_t unit_row = 0;                          // rows in front of (layer, page 0, head)
+  const int page_rows_log2 = a.page_log2;
   auto issue = [&]() {
     if (xa < s1) {
-      const int h = ahead.u / row_tiles % a.Hkv, layer = ahead.u / row_tiles / a.Hkv, len = len_of(a, lens, ahead.b);
+      if (ahead.b != seen_b || ahead.u != seen_u) {
+        seen_b = ahead.b;
+        seen_u = ahead.u;
+        const int lh = ahead.u / row_tiles, layer = lh / a.Hkv;
+        len_a = len_of(a, lens, ahead.b);
+        unit_row = row0_of(a, a.layer0 + layer, 0, lh - layer * a.Hkv);
+      }
+      int pid = -1;
 #pragma unroll
       for (int i = 0; i < TB; ++i) {
         const int tok = (ahead.st * TB + i) * 16;
-        if (tok < len) {
-          const int pid = page_of(a, ahead.b, tok >> a.page_log2);
+        if (tok < len_a) {
+          if (i == 0 || !(tok & (a.page - 1))) {
+            pid = page_of(a, ahead.b, tok >> page_rows_log2);
+            if (pid < 0 && lane == 0) flag(a, KVQ_ERR_PAGE);
+          }
           if (pid >= 0) {
             Tl::load(a, ring_u + in * P::SLOT + i * Tl::BLOCK,
-                     row0_of(a, a.layer0 + layer, pid, h) + (tok & (a.page - 1)));
+                     unit_row + (((size_t)pid * a.Hkv) << page_rows_log2) + (tok & (a.page - 1)));
             have |= 1u << (pending * TB + i);
-          } else if (lane == 0) {
-            flag(a, KVQ_ERR_PAGE);
           }
         }
       }
@@ -227,8 +306,8 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
     __syncthreads();
     const bool whole = unit0 >= s0 && unit0 + cur.n <= s1;
     const int c_first = whole ? me : cta_of_tile(total, workers, unit0), c_last = whole ? me : cta_of_tile(total, workers, unit0 + cur.n - 1);
-    constexpr int REC = D + 2;
-    float* rec = part + (size_t)(2 * me + (unit0 >= s0 ? 1 : 0)) * ROWS * REC;
+    constexpr int REC = ROWS * (D + 2);         // floats of a part: [ROWS][D], maxima, sums of the weights
+    float* rec = part + (size_t)(2 * me + (unit0 >= s0 ? 1 : 0)) * REC;
     for (int e = tid; e < rows * D; e += kThreads) {
       const int j = e / D, c = e % D;
       float m = tops[j], lsum = 0.f, v = 0.f;
@@ -243,10 +322,10 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       if (whole) {
         out[row_at(j) + c] = from_f<T>(m == -INFINITY ? 0.f : v / lsum);
       } else {
-        rec[j * REC + c] = v;
+        rec[e] = v;
         if (c == 0) {
-          rec[j * REC + D] = m;
-          rec[j * REC + D + 1] = lsum;
+          rec[ROWS * D + j] = m;
+          rec[ROWS * D + ROWS + j] = lsum;
         }
       }
     }
@@ -263,20 +342,15 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       __syncthreads();
       if (*shared_int) {
         __threadfence();
-        for (int e = tid; e < rows * D; e += kThreads) {
-          const int j = e / D, c = e % D;
-          float m = -INFINITY, lsum = 0.f, v = 0.f;
-          for (int w = c_first; w <= c_last; ++w) {
-            const float* p = part + ((size_t)(2 * w + (w == c_first ? 1 : 0)) * ROWS + j) * REC;
-            const float mw = __ldcg(p + D), lw = __ldcg(p + D + 1), vw = __ldcg(p + c);
-            if (mw == -INFINITY) continue;
-            const float mn = fmaxf(m, mw), fo = m == -INFINITY ? 0.f : ex2(m - mn), fn = ex2(mw - mn);
-            lsum = lsum * fo + lw * fn;
-            v = v * fo + vw * fn;
-            m = mn;
+        join_parts<P>(part, c_first, c_last, rows, join, tops, [&](int j, int c, float4 v) {
+          T* o = out + row_at(j) + c;
+          if constexpr (F32) {
+            *reinterpret_cast<float4*>(o) = v;
+          } else {
+            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+            *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(h);
           }
-          out[row_at(j) + c] = from_f<T>(m == -INFINITY ? 0.f : v / lsum);
-        }
+        });
       }
     }
     __syncthreads();                            // the queries' operands and the sums may be written anew

@@ -1,4 +1,4 @@
-// The attention tile of the quantised KV cache: one warp, 16 tokens at a time, up to 8 NT query
+// The attention tile of the quantised KV cache: one warp, 16 tokens at a time, 4, 8 or 16 query
 // rows (query heads of one KV head, and query tokens) against all of them.
 //
 // Both products run on mma.sync m16n8k16 (fp16 in, fp32 out) with the CODES as the A operand
@@ -31,6 +31,8 @@
 //   A of the values:  cell r of tokens 2q, 2q + 1, 2q + 8, 2q + 9 (two tokens' words are merged, then
 //                     masked); code pair (2j, 2j + 1) gives rows r, r + 8 of product j;
 //   outputs C:        channels 64 g + 8 r + 2j (+ 1) x columns 2q, 2q + 1.
+// With at most 4 rows, row j is column 2j and the odd columns are left alone: a lane then holds
+// one row instead of two, and everything that is done per score and per output is halved.
 #pragma once
 
 #include "kvq.cuh"
@@ -121,16 +123,18 @@ __device__ __forceinline__ void pair_cell(const uint32_t* w0, const uint32_t* w1
   }
 }
 
-template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
-  static constexpr int BITS = BITS_, D = D_, NT = NT_;
+template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
+  static constexpr int BITS = BITS_, D = D_, ROWS = ROWS_;
   static constexpr bool F32 = F32_;
-  static constexpr int G = D / kGroup, ROW = D * BITS / 8, ROWS = 8 * NT;
+  static constexpr int CP = ROWS == 4 ? 1 : 2;        // rows a lane holds of an 8-column tile
+  static constexpr int NT = ROWS == 16 ? 2 : 1;       // 8-column tiles
+  static constexpr int G = D / kGroup, ROW = D * BITS / 8;
   static constexpr int SP = F32 ? 2 : 1;              // fp16 parts of q and of w
   static constexpr int STEPS = 4 * G;                 // products of a score tile
   static constexpr int BLOCK = 2 * 16 * ROW + 2 * 16 * G * 4;   // bytes of 16 tokens in shared memory
   static constexpr int QFRAG = STEPS * NT * SP * 32 * 8;        // bytes of the queries' B operands
   static constexpr int QMETA = ROWS * (1 + G) * 4;              // f'' and the group sums
-  static constexpr bool QREG = STEPS * NT * SP * 2 <= 32;       // B operands kept in registers
+  static constexpr bool QREG = STEPS * NT * SP * 2 <= 16;       // B operands kept in registers
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   // A score may pass the running maximum by a factor of 2^kSlack in its weight, a value scale leave
   // [2^E, 2^(E+1)) by a factor of kWide either way: w <= 2^(kSlack + 1) kWide kBias < 2^16, and what
@@ -143,53 +147,84 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
   static constexpr float kMid = BITS == 4 ? 8.f : 128.f;
   static constexpr uint32_t kMidLow = BITS == 4 ? 0x80088008u : 0x80808080u, kMidHigh = 0x80808080u;
 
-  float o[NT][G][4][4], ls[NT][G][2], l[NT][2], qs[NT][G][2];
-  float f[NT][2], mneg[NT][2], thr[NT][2];
+  // [..][i * CP + c]: A's row r + 8 i, the lane's c-th column
+  float o[NT][G][4][2 * CP], ls[NT][G][CP], l[NT][CP], qs[NT][G][CP];
+  float f[NT][CP], mneg[NT][CP], thr[NT][CP];
   float unit_inv;                                     // kBias 2^-E, 0 before the first scale
   uint32_t top_s;                                     // the largest scale that needs no new unit (fp16 bits)
   uint2 qr[QREG ? STEPS * NT * SP : 1];
 
+  // The query row of this lane's column (t, c).
+  static __device__ __forceinline__ int row_of(int t, int c) {
+    const int q = threadIdx.x & 3;
+    return CP == 1 ? q : t * 8 + 2 * q + c;
+  }
+
   // ---------------------------------------------------------------- queries
-  // Row j of the tile is query j (of `rows`; the others are zeros).  One warp fills row after row
-  // of the operands: q_row(j) gives its address.  meta: [ROWS] f'', then [ROWS][G] sums.
-  template <class QRow>
-  static __device__ __forceinline__ void prepare(uint8_t* frag, float* meta, int rows, int warp, int nwarps, QRow q_row) {
-    const int lane = threadIdx.x & 31;
-    constexpr int PER = D / 32;   // channels of a lane, consecutive: 2, 4 or 8 (within a cell)
-    for (int j = warp; j < ROWS; j += nwarps) {
-      float x[PER], mx = 0.f, sum = 0.f;
-      const T* src = q_row(j);
+  // Warp w of WARPS takes the rows w, w + WARPS, ... of the tile.  fetch() starts their loads
+  // (rows behind `rows` are zeros), prepare() makes the B operands and meta: [ROWS] f'', then
+  // [ROWS][G] sums.
+  template <int WARPS> struct Queries {
+    static constexpr int PER = D / 32;   // channels of a lane, consecutive (within a cell)
+    static constexpr int MINE = (ROWS + WARPS - 1) / WARPS;
+    __align__(16) T raw[MINE][PER];
+    template <class QRow> __device__ __forceinline__ void fetch(int rows, int warp, QRow q_row) {
+      const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        x[i] = j < rows ? to_f<T>(src[lane * PER + i]) : 0.f;
-        mx = fmaxf(mx, fabsf(x[i]));
-        sum += x[i];
-      }
-      mx = warp_max(mx);
-      // a power of two: 2^13 <= mx sigma < 2^14 (1 for a row of zeros, or with an infinity)
-      const int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      float sigma = 1.f;
-      if (e > -127 && e < 128) sigma = ldexpf(1.f, min(13 - e, 100));
+      for (int k = 0; k < MINE; ++k) {
+        const int j = warp + k * WARPS;
 #pragma unroll
-      for (int o = 16 / G; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);   // 32 / G lanes hold a group
-      if (lane == 0) meta[j] = kLog2e * rsqrtf((float)D) * (16777216.f / sigma);
-      if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * sigma * (1.f / 16777216.f);
+        for (int i = 0; i < PER; ++i) raw[k][i] = from_f<T>(0.f);
+        if (j < rows) {
+          const T* src = q_row(j) + lane * PER;
+          constexpr int BY = PER * (int)sizeof(T);
+          if constexpr (BY == 4) *reinterpret_cast<uint32_t*>(raw[k]) = __ldg(reinterpret_cast<const uint32_t*>(src));
+          else if constexpr (BY == 8) *reinterpret_cast<uint2*>(raw[k]) = __ldg(reinterpret_cast<const uint2*>(src));
+          else
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int c = lane * PER + i, g = c / 64, w = c % 64 / 8, code = c % 8;
-        const int half = BITS == 4 ? code % 4 / 2 : code / 4, hi = BITS == 4 ? code / 4 : code % 4 / 2, reg = code % 2;
-        float y = x[i] * sigma;
-        if (BITS == 4 && reg) y *= 0.0625f;
-        const int step = (g * 2 + w % 2) * 2 + half;
-        __half* at = reinterpret_cast<__half*>(frag) + ((((step * NT + j / 8) * SP) * 32 + j % 8 * 4 + w / 2) * 2 + reg) * 2 + hi;
-        const __half h = __float2half_rn(y);
-        at[0] = h;
-        if constexpr (F32) at[32 * 4] = __float2half_rn(y - __half2float(h));
+            for (int i = 0; i < BY / 16; ++i) reinterpret_cast<uint4*>(raw[k])[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        }
       }
     }
-  }
+    __device__ __forceinline__ void prepare(uint8_t* frag, float* meta, int warp) const {
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) {
+        const int j = warp + k * WARPS;
+        if (j >= ROWS) break;
+        float x[PER], mx = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          x[i] = to_f<T>(raw[k][i]);
+          mx = fmaxf(mx, fabsf(x[i]));
+          sum += x[i];
+        }
+        mx = warp_max(mx);
+        // a power of two: 2^13 <= mx sigma < 2^14 (1 for a row of zeros, or with an infinity)
+        const int e = (int)(__float_as_uint(mx) >> 23) - 127;
+        const float sigma = e > -127 && e < 128 ? __uint_as_float((unsigned)(min(13 - e, 100) + 127) << 23) : 1.f;
+#pragma unroll
+        for (int i = 16 / G; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);   // 32 / G lanes hold a group
+        if (lane == 0) meta[j] = kLog2e * rsqrtf((float)D) * (16777216.f / sigma);
+        if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * sigma * (1.f / 16777216.f);
+        const int col = CP == 1 ? 2 * j : j % 8, tile = CP == 1 ? 0 : j / 8;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int c = lane * PER + i, g = c / 64, w = c % 64 / 8, code = c % 8;
+          const int half = BITS == 4 ? code % 4 / 2 : code / 4, hi = BITS == 4 ? code / 4 : code % 4 / 2, reg = code % 2;
+          float y = x[i] * sigma;
+          if (BITS == 4 && reg) y *= 0.0625f;
+          const int step = (g * 2 + w % 2) * 2 + half;
+          __half* at = reinterpret_cast<__half*>(frag) + ((((step * NT + tile) * SP) * 32 + col * 4 + w / 2) * 2 + reg) * 2 + hi;
+          const __half h = __float2half_rn(y);
+          at[0] = h;
+          if constexpr (F32) at[32 * 4] = __float2half_rn(y - __half2float(h));
+        }
+      }
+    }
+  };
   __device__ __forceinline__ void begin(const uint8_t* frag, const float* meta) {
-    const int lane = threadIdx.x & 31, q = lane & 3;
+    const int lane = threadIdx.x & 31;
     if constexpr (QREG) {
 #pragma unroll
       for (int i = 0; i < STEPS * NT * SP; ++i) qr[i] = reinterpret_cast<const uint2*>(frag)[i * 32 + lane];
@@ -197,8 +232,8 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int j = t * 8 + 2 * q + c;
+      for (int c = 0; c < CP; ++c) {
+        const int j = row_of(t, c);
         f[t][c] = meta[j];
         mneg[t][c] = 0.f;
         thr[t][c] = -INFINITY;
@@ -208,7 +243,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
           qs[t][g][c] = meta[ROWS + j * G + g];
           ls[t][g][c] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[t][g][k][c] = o[t][g][k][2 + c] = 0.f;
+          for (int k = 0; k < 4; ++k) o[t][g][k][c] = o[t][g][k][CP + c] = 0.f;
         }
       }
     unit_inv = 0.f;
@@ -238,18 +273,18 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
   }
 
   // ---------------------------------------------------------------- 16 TB tokens
-  // Token t of block i of this step has place tok + 16 i + t; column c of tile nt sees places below
-  // lim[nt][c].  EDGE: some place is masked (or block i is not there: bit i of `have` clear).
+  // Token t of block i has place tok + 16 i + t; column (t, c) sees the places below lim[t][c].
+  // EDGE: some place is masked; what such a place holds (anything, NaN too) plays no part.
   template <int TB, bool EDGE>
-  __device__ __forceinline__ void step(const uint8_t* slot, const uint8_t* frag, int tok, const int (&lim)[NT][2], unsigned have) {
+  __device__ __forceinline__ void step(const uint8_t* slot, const uint8_t* frag, int tok, const int (&lim)[NT][CP]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-    constexpr int CODE = 16 * ROW, META = 16 * G * 4;
-    float x[TB][NT][4];
+    constexpr int CODE = 16 * ROW, META = 16 * G * 4, CW = BITS / 4;
+    float x[TB][NT][2 * CP];
     // scores, in units of 1 / f''
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
       const uint8_t* base = slot + b * BLOCK;
-      uint32_t k0[2 * G * BITS / 4], k1[2 * G * BITS / 4];
+      uint32_t k0[2 * G * CW], k1[2 * G * CW];
       lds<2 * G * BITS>(k0, base + r * ROW + q * 2 * G * BITS);
       lds<2 * G * BITS>(k1, base + (r + 8) * ROW + q * 2 * G * BITS);
       uint32_t m0[G], m1[G];
@@ -258,7 +293,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[b][t][k] = 0.f;
+        for (int k = 0; k < 2 * CP; ++k) x[b][t][k] = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float acc[NT][4];
@@ -271,8 +306,8 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t a0, a1, a2, a3;
-            half_cell<BITS>(k0 + (e * G + g) * (BITS / 4), h, a0, a2);
-            half_cell<BITS>(k1 + (e * G + g) * (BITS / 4), h, a1, a3);
+            half_cell<BITS>(k0 + (e * G + g) * CW, h, a0, a2);
+            half_cell<BITS>(k1 + (e * G + g) * CW, h, a1, a3);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -283,17 +318,20 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 u = k < 2 ? u0 : u1;
-            x[b][t][k] = fmaf(u.x, acc[t][k], fmaf(u.y, qs[t][g][k & 1], x[b][t][k]));
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < CP; ++c) {
+              const float2 u = i ? u1 : u0;
+              float& y = x[b][t][i * CP + c];
+              y = fmaf(u.x, acc[t][2 * i + c], fmaf(u.y, qs[t][g][c], y));
+            }
       }
       if constexpr (EDGE) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (!(have >> b & 1) || tok + 16 * b + r + (k < 2 ? 0 : 8) >= lim[t][k & 1]) x[b][t][k] = -INFINITY;
+          for (int k = 0; k < 2 * CP; ++k)
+            if (tok + 16 * b + r + 8 * (k / CP) >= lim[t][k % CP]) x[b][t][k] = -INFINITY;
       }
     }
     // value scales and offsets of the tokens r, r + 8
@@ -306,8 +344,10 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
         if constexpr (EDGE) {
           int most = lim[0][0];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) most = max(most, max(lim[t][0], lim[t][1]));
-          if (!(have >> b & 1) || tok + 16 * b + r + 8 * i >= most)
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < CP; ++c) most = max(most, lim[t][c]);
+          if (tok + 16 * b + r + 8 * i >= most)
 #pragma unroll
             for (int g = 0; g < G; ++g) vm[b][i][g] = 0;
         }
@@ -320,20 +360,19 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) high |= x[b][t][k] > thr[t][k & 1];
+        for (int k = 0; k < 2 * CP; ++k) high |= x[b][t][k] > thr[t][k % CP];
     if (__any_sync(kFull, high)) move<TB>(x, most_s & 0xffffu);
-    // weights: p in x's place, the offsets' part, the sum of the weights
+    // weights: p in x's place, the sum of the weights
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float p = ex2(fmaf(x[b][t][k], f[t][k & 1], mneg[t][k & 1]));
+        for (int k = 0; k < 2 * CP; ++k) {
+          const float p = ex2(fmaf(x[b][t][k], f[t][k % CP], mneg[t][k % CP]));
           x[b][t][k] = p;
-          l[t][k & 1] += p;
+          l[t][k % CP] += p;
         }
-    constexpr int CW = BITS / 4;
     uint32_t v[TB][4][G * CW];   // cell r of the tokens 2q, 2q + 1, 2q + 8, 2q + 9
 #pragma unroll
     for (int b = 0; b < TB; ++b)
@@ -349,34 +388,37 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
         for (int k = 0; k < 4; ++k) base[t][k] = 0.f;
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][0][g]));
-        float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][1][g]));
-        u0 = make_float2(u0.x * unit_inv, fmaf(kMid, u0.x, u0.y));
-        u1 = make_float2(u1.x * unit_inv, fmaf(kMid, u1.x, u1.y));
+        float2 u[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][i][g]));
+          u[i] = make_float2(m.x * unit_inv, fmaf(kMid, m.x, m.y));
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float y[4];
+          float y[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 u = k < 2 ? u0 : u1;
-            const float p = x[b][t][k];
-            y[k] = p * u.x;
-            float z = p * u.y;
-            if constexpr (EDGE) {   // a place this column does not see may hold anything
-              const bool seen = (have >> b & 1) && tok + 16 * b + r + (k < 2 ? 0 : 8) < lim[t][k & 1];
-              y[k] = seen ? y[k] : 0.f;
-              z = seen ? z : 0.f;
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < CP; ++c) {
+              const float p = x[b][t][i * CP + c];
+              y[i][c] = p * u[i].x;
+              if constexpr (EDGE) {   // a place this column does not see may hold anything
+                const bool seen = tok + 16 * b + r + 8 * i < lim[t][c];
+                y[i][c] = seen ? y[i][c] : 0.f;
+                ls[t][g][c] += seen ? p * u[i].y : 0.f;
+              } else {
+                ls[t][g][c] = fmaf(p, u[i].y, ls[t][g][c]);
+              }
             }
-            ls[t][g][k & 1] += z;
-          }
           if constexpr (F32) {
             uint32_t h0, h1, l0, l1;
-            split_h2(y[0], y[1], h0, l0);
-            split_h2(y[2], y[3], h1, l1);
+            split_h2(y[0][0], y[0][1], h0, l0);
+            split_h2(y[1][0], y[1][1], h1, l1);
             w[b][t][0] = make_uint2(trans8x8(h0), trans8x8(h1));
             w[b][t][SP - 1] = make_uint2(trans8x8(l0), trans8x8(l1));
           } else {
-            w[b][t][0] = make_uint2(trans8x8(pack_h2(y[0], y[1])), trans8x8(pack_h2(y[2], y[3])));
+            w[b][t][0] = make_uint2(trans8x8(pack_h2(y[0][0], y[0][1])), trans8x8(pack_h2(y[1][0], y[1][1])));
           }
 #pragma unroll
           for (int i = SP - 1; i >= 0; --i) mma_f16(base[t], kMidLow, kMidHigh, kMidLow, kMidHigh, w[b][t][i]);
@@ -402,7 +444,9 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[t][g][j][k] += acc[t][k];
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < CP; ++c) o[t][g][j][i * CP + c] += acc[t][2 * i + c];
       }
     }
   }
@@ -410,7 +454,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
   // A score passed the running maximum, or a value scale its unit's room: both anew.  A unit that
   // has become far too large is made smaller here as well: the scales it was made for have lost
   // their weight only if the maximum has moved.
-  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][4], uint32_t most_s) {
+  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][2 * CP], uint32_t most_s) {
     const uint32_t sb = __reduce_max_sync(kFull, most_s);
     const float s = __half2float(__ushort_as_half((unsigned short)sb));
     float scale = 1.f;
@@ -423,10 +467,10 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < CP; ++c) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < TB; ++b) mx = fmaxf(mx, fmaxf(x[b][t][c], x[b][t][2 + c]));
+        for (int b = 0; b < TB; ++b) mx = fmaxf(mx, fmaxf(x[b][t][c], x[b][t][CP + c]));
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, i));
         float alpha = 1.f;
@@ -444,7 +488,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             o[t][g][j][c] *= both;
-            o[t][g][j][2 + c] *= both;
+            o[t][g][j][CP + c] *= both;
           }
         }
       }
@@ -458,7 +502,7 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < CP; ++c)
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) {
           l[t][c] += __shfl_xor_sync(kFull, l[t][c], i);
@@ -466,10 +510,36 @@ template <int BITS_, int D_, int NT_, bool F32_> struct Tile {
           for (int g = 0; g < G; ++g) ls[t][g][c] += __shfl_xor_sync(kFull, ls[t][g][c], i);
         }
   }
-  // Output of channel 64 g + 8 r + 2 j + i, column c (unnormalised), after reduce().
-  __device__ __forceinline__ float value(int t, int g, int j, int i, int c) const {
-    const float un = unit_inv == 0.f ? 0.f : (i && BITS == 4 ? 1048576.f : 16777216.f) / unit_inv;
-    return fmaf(o[t][g][j][2 * i + c], un, ls[t][g][c]);
+  // Leaves the maxima and the sums of the weights of this warp's rows (after reduce()).
+  __device__ __forceinline__ void store_tops(float* tops, float* sums) const {
+    if ((threadIdx.x & 31) < 4) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < CP; ++c) {
+          tops[row_of(t, c)] = top(t, c);
+          sums[row_of(t, c)] = l[t][c];
+        }
+    }
+  }
+  // The unnormalised outputs [ROWS][D], times weight(row) (0: left out; its sums may be anything).
+  template <class Weight> __device__ __forceinline__ void store_out(float* to, Weight weight) const {
+    const int r = (threadIdx.x & 31) >> 2;
+    const float u0 = unit_inv == 0.f ? 0.f : 16777216.f / unit_inv, u1 = BITS == 4 ? u0 * 0.0625f : u0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < CP; ++c) {
+        const int j = row_of(t, c);
+        const float w = weight(j);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = make_float2(fmaf(o[t][g][k][c], u0, ls[t][g][c]), fmaf(o[t][g][k][CP + c], u1, ls[t][g][c]));
+            *reinterpret_cast<float2*>(to + j * D + 64 * g + 8 * r + 2 * k) = w == 0.f ? make_float2(0.f, 0.f) : make_float2(v.x * w, v.y * w);
+          }
+      }
   }
 };
 

@@ -18,21 +18,48 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxWorkers = 640;
+#ifndef KVQ_LEAST
+#define KVQ_LEAST 8
+#endif
+constexpr unsigned kLeast = KVQ_LEAST;
 constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are fewer
 
-template <int BITS, int D, int NT, bool F32> struct Plan {
-  using Tl = Tile<BITS, D, NT, F32>;
-  static constexpr int TB = Tl::BLOCK <= 2304 ? 2 : 1;      // 16-token blocks of a step
+template <int BITS, int D, int ROWS, bool F32> struct Plan {
+  using Tl = Tile<BITS, D, ROWS, F32>;
+  #ifdef KVQ_TB
+  static constexpr int TB = KVQ_TB;
+#else
+  static constexpr int TB = Tl::BLOCK <= 2304 ? 2 : 1;
+#endif      // 16-token blocks of a step
   static constexpr int SLOT = TB * Tl::BLOCK;
+  #ifdef KVQ_STAGES
+  static constexpr int STAGES = KVQ_STAGES;
+#else
   static constexpr int STAGES = SLOT > 4608 ? 2 : 3;
+#endif
   static constexpr int JOIN = kWarps * Tl::ROWS * D * 4;    // the warps' sums
   static constexpr int RING = kWarps * STAGES * SLOT;
   static constexpr int SMEM = RING + JOIN + Tl::QFRAG + Tl::QMETA + kWarps * Tl::ROWS * 8 + 16;
+  #ifdef KVQ_MINB
+  static constexpr int MINB = KVQ_MINB;
+#else
   static constexpr int MINB = SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);
+#endif
 };
 
 struct Walk {   // a place on the line of steps
   int b, u, st, n;   // sequence, unit inside it, step inside the unit, steps of its units
+};
+
+// `total` steps cut into `parts` pieces (parts <= total), the first total % parts one longer.
+struct Cut {
+  unsigned each, longer;
+  __device__ Cut(unsigned total, unsigned parts) : each(total / parts), longer(total % parts) {}
+  __device__ __forceinline__ unsigned begin(unsigned c) const { return c * each + min(c, longer); }
+  __device__ __forceinline__ int piece_of(unsigned x) const {
+    const unsigned turn = longer * (each + 1);
+    return x < turn ? x / (each + 1) : longer + (x - turn) / each;
+  }
 };
 
 template <class P> struct Line {
@@ -41,31 +68,39 @@ template <class P> struct Line {
   int U;   // units of a sequence
   static constexpr int TOK = 16 * P::TB;
   __device__ __forceinline__ int steps(int b) const { return max(1, (len_of(a, lens, b) + TOK - 1) / TOK); }
-  __device__ long long total() const {   // the same on every lane
+  // The steps of all units (the same on every lane; below 2^31, the host checks).  Where there are at
+  // most 32 sequences, `scan` is what at() needs: a lane's steps and their running sum.
+  __device__ __forceinline__ unsigned total(uint2& scan) const {
     const int lane = threadIdx.x & 31;
-    long long t = 0;
-    for (int b = lane; b < a.B; b += 32) t += steps(b);
+    unsigned t = 0;
+    for (int b = lane; b < a.B; b += 32) t += steps(b) * U;
+    unsigned inc = t;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-    return t * U;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += y;
+    }
+    scan = make_uint2(t, inc);
+    return __shfl_sync(kFull, inc, 31);
   }
-  __device__ Walk at(long long x) const {   // 0 <= x < total
+  __device__ __forceinline__ Walk at(unsigned x, uint2 scan) const {   // 0 <= x < total
     const int lane = threadIdx.x & 31;
-    long long before = 0;
+    unsigned before = 0, n = scan.x, inc = scan.y;
     for (int b0 = 0;; b0 += 32) {
-      const int b = b0 + lane, n = b < a.B ? steps(b) : 0;
-      long long inc = n;
+      if (a.B > 32) {
+        n = b0 + lane < a.B ? steps(b0 + lane) * U : 0;
+        inc = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned y = __shfl_up_sync(kFull, inc, o);
+          if (lane >= o) inc += y;
+        }
       }
-      const unsigned past = __ballot_sync(kFull, (before + inc) * U > x);
+      const unsigned past = __ballot_sync(kFull, before + inc > x);
       if (past) {
         const int w = __ffs(past) - 1;
-        const long long start = (before + __shfl_sync(kFull, inc - n, w)) * U;
-        const int nn = __shfl_sync(kFull, n, w), rel = (int)((x - start) / nn);
-        return Walk{b0 + w, rel, (int)(x - start - (long long)rel * nn), nn};
+        const unsigned in = x - (before + __shfl_sync(kFull, inc - n, w)), nn = __shfl_sync(kFull, n, w) / U, u = in / nn;
+        return Walk{b0 + w, (int)u, (int)(in - u * nn), (int)nn};
       }
       before += __shfl_sync(kFull, inc, 31);
     }
@@ -89,10 +124,10 @@ template <class P> struct Line {
 
 // The parts of a unit (CTAs c_first .. c_last), joined in their order.  The weights of a chunk of
 // parts are computed side by side, then each thread sums four channels over them with its loads in
-// flight together.  wt: [kChunk][ROWS] floats; norm: [ROWS] maxima, then [ROWS] sums.
+// flight together.  wt: [2][kChunk][ROWS] floats; norm: [ROWS] maxima, then [ROWS] sums.
 template <class P, class Store>
 __device__ __forceinline__ void join_parts(const float* part, int c_first, int c_last, int rows, float* wt, float* norm, Store store) {
-  constexpr int ROWS = P::Tl::ROWS, D = P::Tl::D, REC = ROWS * (D + 2), kChunk = P::JOIN / 4 / ROWS;
+  constexpr int ROWS = P::Tl::ROWS, D = P::Tl::D, REC = ROWS * (D + 2), kChunk = P::JOIN / 8 / ROWS;
   static_assert(2 * ROWS <= kThreads, "rows");
   const int tid = threadIdx.x, n = c_last - c_first + 1;
   auto at = [&](int i) { return part + (size_t)(2 * (c_first + i) + (i == 0 ? 1 : 0)) * REC; };
@@ -100,6 +135,7 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
   constexpr int PER = kThreads / ROWS;
   const int jr = tid % ROWS, pr = tid / ROWS;
   float m = -INFINITY;
+#pragma unroll 4
   for (int i = pr; i < n; i += PER) m = fmaxf(m, __ldcg(at(i) + ROWS * D + jr));
   __syncthreads();
   wt[pr * ROWS + jr] = m;
@@ -116,14 +152,18 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
   for (int i0 = 0; i0 < n; i0 += kChunk) {
     const int nc = min(kChunk, n - i0);
     __syncthreads();
+    float* wl = wt + kChunk * ROWS;
+#pragma unroll 4
     for (int e = tid; e < nc * ROWS; e += kThreads) {
-      const float mj = norm[e % ROWS], mp = __ldcg(at(i0 + e / ROWS) + ROWS * D + e % ROWS);
+      const float* p = at(i0 + e / ROWS) + ROWS * D + e % ROWS;
+      const float mj = norm[e % ROWS], mp = __ldcg(p), lp = __ldcg(p + ROWS);
       wt[e] = mp == -INFINITY ? 0.f : ex2(mp - mj);
+      wl[e] = mp == -INFINITY ? 0.f : lp * wt[e];
     }
     __syncthreads();
     if (tid < ROWS) {
       float l = norm[ROWS + tid];
-      for (int i = 0; i < nc; ++i) l = fmaf(wt[i * ROWS + tid], __ldcg(at(i0 + i) + ROWS * D + ROWS + tid), l);
+      for (int i = 0; i < nc; ++i) l += wl[i * ROWS + tid];
       norm[ROWS + tid] = l;
     }
 #pragma unroll
@@ -154,14 +194,14 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
   }
 }
 
-template <int BITS, int D, int NT, bool F32>
-__global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT, F32>::MINB)
+template <int BITS, int D, int ROWS, bool F32>
+__global__ void __launch_bounds__(kThreads, Plan<BITS, D, ROWS, F32>::MINB)
 decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
               unsigned* __restrict__ arrived, float* __restrict__ part) {
-  using P = Plan<BITS, D, NT, F32>;
+  using P = Plan<BITS, D, ROWS, F32>;
   using Tl = typename P::Tl;
   using T = typename Tl::T;
-  constexpr int ROWS = Tl::ROWS, G = Tl::G, TB = P::TB;
+  constexpr int TB = P::TB;
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* frag = sm + P::RING;
   float* join = reinterpret_cast<float*>(frag + Tl::QFRAG);
@@ -173,65 +213,81 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   T* out = static_cast<T*>(outv);
   const int rows_all = a.n * a.g;
   const Line<P> line{a, lens, a.n_layers * a.Hkv * row_tiles};
-  const long long total = line.total();
-  // at least one step per warp where there are few
-  const long long want = (total + kWarps - 1) / kWarps;
+  uint2 scan;
+  const unsigned total = line.total(scan);
+  // a piece of fewer steps than kLeast would be gone before the joining of its parts
+  const unsigned want = (total + kLeast - 1) / kLeast;
   const int workers = want < gridDim.x ? (int)want : gridDim.x, me = blockIdx.x;
   if (me >= workers) return;
   if (me == 0)
     for (int b = tid; b < a.B; b += kThreads)
       if (len_bad(a, lens, b)) flag(a, KVQ_ERR_RANGE);
-  const long long s0 = tile_begin(total, workers, me), s1 = tile_begin(total, workers, me + 1);
-  Walk cur = line.at(s0), ahead = cur;
+  const Cut cut(total, workers);
+  const unsigned s0 = cut.begin(me), s1 = cut.begin(me + 1);
+  Walk cur = line.at(s0, scan), ahead = cur;
   line.forward(ahead, warp);
-  long long xa = s0 + warp;                     // the next step to load
+  unsigned xa = s0 + warp;                      // the next step to load
   uint8_t* ring = sm + warp * P::STAGES * P::SLOT;
   const uint32_t ring_u = smem_u32(ring);
   unsigned have = 0;                            // TB bits per step in flight: blocks that are there
   int pending = 0, in = 0, rd = 0;
-  // what the loads of a unit need, made anew when `ahead` enters another one
-  int seen_b = -1, seen_u = -1, len_a = 0;
-  size_t unit_row = 0;                          // rows in front of (layer, page 0, head)
-  const int page_rows_log2 = a.page_log2;
+  // Loads run two calls behind the walk: lookup() asks the table for the pages of the next step,
+  // issue() starts the copies of the step looked up before and looks up the one after it.
+  int seen_b = -1, seen_u = -1, len_a = 0, tok_a = -1, pid_a[TB];
+  size_t unit_row = 0, row_a = 0;               // rows in front of (layer, page 0, head)
+  auto lookup = [&]() {
+    tok_a = -1;
+    if (xa >= s1) return;
+    if (ahead.b != seen_b || ahead.u != seen_u) {   // another unit
+      seen_b = ahead.b;
+      seen_u = ahead.u;
+      const int lh = ahead.u / row_tiles, layer = lh / a.Hkv;
+      len_a = len_of(a, lens, ahead.b);
+      unit_row = row0_of(a, a.layer0 + layer, 0, lh - layer * a.Hkv);
+    }
+    row_a = unit_row;
+    tok_a = ahead.st * Line<P>::TOK;
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+      const int tok = tok_a + 16 * i;
+      if (i > 0 && (tok & (a.page - 1))) pid_a[i] = tok < len_a ? pid_a[i - 1] : -2;
+      else pid_a[i] = tok < len_a ? page_of(a, ahead.b, tok >> a.page_log2) : -2;
+    }
+    xa += kWarps;
+    line.forward(ahead, kWarps);
+  };
   auto issue = [&]() {
-    if (xa < s1) {
-      if (ahead.b != seen_b || ahead.u != seen_u) {
-        seen_b = ahead.b;
-        seen_u = ahead.u;
-        const int lh = ahead.u / row_tiles, layer = lh / a.Hkv;
-        len_a = len_of(a, lens, ahead.b);
-        unit_row = row0_of(a, a.layer0 + layer, 0, lh - layer * a.Hkv);
-      }
-      int pid = -1;
+    const int tok = tok_a;
+    if (tok >= 0) {
+      int pid[TB];
+#pragma unroll
+      for (int i = 0; i < TB; ++i) pid[i] = pid_a[i];
+      const size_t row = row_a + (tok & (a.page - 1));
+      lookup();
 #pragma unroll
       for (int i = 0; i < TB; ++i) {
-        const int tok = (ahead.st * TB + i) * 16;
-        if (tok < len_a) {
-          if (i == 0 || !(tok & (a.page - 1))) {
-            pid = page_of(a, ahead.b, tok >> page_rows_log2);
-            if (pid < 0 && lane == 0) flag(a, KVQ_ERR_PAGE);
-          }
-          if (pid >= 0) {
-            Tl::load(a, ring_u + in * P::SLOT + i * Tl::BLOCK,
-                     unit_row + (((size_t)pid * a.Hkv) << page_rows_log2) + (tok & (a.page - 1)));
-            have |= 1u << (pending * TB + i);
-          }
+        if (pid[i] >= 0) {
+          // block i of a step lies in the page of block 0, or at the start of its own (page = 16)
+          const size_t at = row + (((size_t)pid[i] * a.Hkv) << a.page_log2) + (a.page > 16 ? 16 * i : 0);
+          Tl::load(a, ring_u + in * P::SLOT + i * Tl::BLOCK, at);
+          have |= 1u << (pending * TB + i);
+        } else if (pid[i] == -1 && lane == 0) {
+          flag(a, KVQ_ERR_PAGE);
         }
       }
       ++pending;
       in = in + 1 == P::STAGES ? 0 : in + 1;
-      xa += kWarps;
-      line.forward(ahead, kWarps);
     }
     cp_commit();
   };
-#pragma unroll
-  for (int i = 0; i < P::STAGES - 1; ++i) issue();
+  lookup();
 
   Tl tile;
-  for (long long x = s0; x < s1;) {             // a unit's part at a time
-    const long long x1 = min(s1, x + (cur.n - cur.st)), unit0 = x - cur.st;
-    const int rt = cur.u % row_tiles, h = cur.u / row_tiles % a.Hkv, layer = cur.u / row_tiles / a.Hkv;
+  bool first = true;
+  for (unsigned x = s0; x < s1;) {              // a unit's part at a time
+    const unsigned x1 = min(s1, x + (cur.n - cur.st));
+    const int unit0 = (int)x - cur.st;          // its first step
+    const int rt = cur.u % row_tiles, lh = cur.u / row_tiles, layer = lh / a.Hkv, h = lh - layer * a.Hkv;
     const int row_base = rt * ROWS, rows = min(ROWS, rows_all - row_base), len = len_of(a, lens, cur.b);
     // row j of the tile: query token (row_base + j) / g, head (row_base + j) % g of the KV head
     const size_t qbase = ((size_t)layer * a.B + cur.b) * a.n;
@@ -239,17 +295,23 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       const int i = (row_base + j) / a.g, jj = (row_base + j) % a.g;
       return ((qbase + i) * a.Hq + (size_t)h * a.g + jj) * D;
     };
-    Tl::prepare(frag, meta, rows, warp, kWarps, [&](int j) { return q + (j < rows ? row_at(j) : 0); });
+    {
+      typename Tl::template Queries<kWarps> qr;
+      qr.fetch(rows, warp, [&](int j) { return q + row_at(j); });
+      if (first) {
+#pragma unroll 1
+        for (int i = 0; i < P::STAGES - 1; ++i) issue();
+        first = false;
+      }
+      qr.prepare(frag, meta, warp);
+    }
     __syncthreads();
     tile.begin(frag, meta);
-    int lim[NT][2];
+    int lim[Tl::NT][Tl::CP];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < Tl::NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int j = min(t * 8 + 2 * (lane & 3) + c, rows - 1);
-        lim[t][c] = len - a.n + 1 + (row_base + j) / a.g;
-      }
+      for (int c = 0; c < Tl::CP; ++c) lim[t][c] = len - a.n + 1 + (row_base + min(Tl::row_of(t, c), rows - 1)) / a.g;
     const int least = len - a.n + 1 + row_base / a.g;
     // this warp's steps of the part: x = s0 + warp modulo kWarps
     int st = cur.st + (int)((warp - (x - s0) % kWarps + kWarps) % kWarps);
@@ -262,52 +324,32 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       --pending;
       const uint8_t* slot = ring + rd * P::SLOT;
       const int tok = st * Line<P>::TOK;
-      if (there == (1u << TB) - 1 && tok + Line<P>::TOK <= least) tile.template step<TB, false>(slot, frag, tok, lim, there);
-      else tile.template step<TB, true>(slot, frag, tok, lim, there);
+      if (there == (1u << TB) - 1 && tok + Line<P>::TOK <= least) {
+        tile.template step<TB, false>(slot, frag, tok, lim);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < TB; ++i)            // nothing to see in a block that is not there
+          if (there >> i & 1) tile.template step<1, true>(slot + i * Tl::BLOCK, frag, tok + 16 * i, lim);
+      }
       rd = rd + 1 == P::STAGES ? 0 : rd + 1;
       __syncwarp();
       issue();
     }
     // join the warps: common maximum, scaled sums, channels added warp by warp
     tile.reduce();
-    if (lane < 4) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int j = t * 8 + 2 * lane + c;
-          tops[warp * ROWS + j] = tile.top(t, c);
-          tops[(kWarps + warp) * ROWS + j] = tile.l[t][c];
-        }
-    }
+    tile.store_tops(tops + warp * ROWS, tops + (kWarps + warp) * ROWS);
     __syncthreads();
-    {
-      const int r = lane >> 2, qd = lane & 3;
+    tile.store_out(join + warp * ROWS * D, [&](int j) {
+      float m = tops[j];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int j = t * 8 + 2 * qd + c;
-          float m = tops[j];
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) m = fmaxf(m, tops[w * ROWS + j]);
-          const float mine = tops[warp * ROWS + j], fac = mine == -INFINITY ? 0.f : ex2(mine - m);
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float2 v = make_float2(tile.value(t, g, k, 0, c), tile.value(t, g, k, 1, c));
-              if (fac == 0.f) v = make_float2(0.f, 0.f);   // no token: its sums are zeros times anything
-              else { v.x *= fac; v.y *= fac; }
-              *reinterpret_cast<float2*>(join + (size_t)(warp * ROWS + j) * D + 64 * g + 8 * r + 2 * k) = v;
-            }
-        }
-    }
+      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, tops[w * ROWS + j]);
+      const float mine = tops[warp * ROWS + j];
+      return mine == -INFINITY ? 0.f : ex2(mine - m);
+    });
     __syncthreads();
-    const bool whole = unit0 >= s0 && unit0 + cur.n <= s1;
-    const int c_first = whole ? me : cta_of_tile(total, workers, unit0), c_last = whole ? me : cta_of_tile(total, workers, unit0 + cur.n - 1);
+    const bool starts = unit0 >= (int)s0, whole = starts && unit0 + cur.n <= (int)s1;
     constexpr int REC = ROWS * (D + 2);         // floats of a part: [ROWS][D], maxima, sums of the weights
-    float* rec = part + (size_t)(2 * me + (unit0 >= s0 ? 1 : 0)) * REC;
+    float* rec = part + (size_t)(2 * me + (starts ? 1 : 0)) * REC;
     for (int e = tid; e < rows * D; e += kThreads) {
       const int j = e / D, c = e % D;
       float m = tops[j], lsum = 0.f, v = 0.f;
@@ -331,6 +373,7 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
     }
     if (!whole) {
       // the last CTA of the unit to come joins all parts, in their order
+      const int c_first = cut.piece_of(unit0), c_last = cut.piece_of(unit0 + cur.n - 1);
       __threadfence();
       __syncthreads();
       unsigned* cnt = arrived + (size_t)cur.b * line.U + cur.u;
@@ -361,12 +404,16 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   cp_wait<0>();
 }
 
-// Query rows of a tile: 16 where there are more than 8 and the sums fit the registers (d <= 128).
-int rows_tile(const Args& a) { return a.d <= 128 && a.n * a.g > 8 ? 16 : 8; }
+// Query rows of a tile: the fewest of 4, 8 and 16 that hold all, 16 only where the sums fit the
+// registers (d <= 128).
+int rows_tile(const Args& a) {
+  const int rows = a.n * a.g;
+  return rows <= 4 ? 4 : (a.d <= 128 && rows > 8 ? 16 : 8);
+}
 
-template <int BITS, int D, int NT, bool F32>
+template <int BITS, int D, int ROWS, bool F32>
 cudaError_t go(const Args& a, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s) {
-  using P = Plan<BITS, D, NT, F32>;
+  using P = Plan<BITS, D, ROWS, F32>;
   // per device: the kernel's attribute and the CTAs that are resident at once
   static int workers[64] = {0};
   int dev = 0;
@@ -375,28 +422,42 @@ cudaError_t go(const Args& a, const void* q, const int32_t* lens, void* out, voi
   int w = dev < 64 ? workers[dev] : 0;
   if (!w) {
     int sm = 0, per = 0;
-    if ((e = cudaFuncSetAttribute(decode_kernel<BITS, D, NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(decode_kernel<BITS, D, ROWS, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, decode_kernel<BITS, D, NT, F32>, kThreads, P::SMEM)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, decode_kernel<BITS, D, ROWS, F32>, kThreads, P::SMEM)) != cudaSuccess) return e;
     w = sm * (per < 1 ? 1 : per);
     if (w > kMaxWorkers) w = kMaxWorkers;
     if (dev < 64) workers[dev] = w;
   }
-  static_assert((size_t)2 * kMaxWorkers * 8 * NT * (D + 2) * 4 <= kPartBytes, "parts");
+  static_assert((size_t)2 * kMaxWorkers * ROWS * (D + 2) * 4 <= kPartBytes, "parts");
   // the parts first: the counters of every kind of call start at one place and stay zero between calls
   float* part = static_cast<float*>(ws);
   unsigned* arrived = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kPartBytes);
-  const int tiles = (a.n * a.g + 8 * NT - 1) / (8 * NT);
-  decode_kernel<BITS, D, NT, F32><<<w, kThreads, P::SMEM, s>>>(a, tiles, q, lens, out, arrived, part);
+  const int tiles = (a.n * a.g + ROWS - 1) / ROWS;
+  // the line of steps is counted in 32 bits
+  if ((double)a.n_layers * a.B * a.Hkv * tiles * ((((double)a.max_pages * a.page) + 16 * P::TB - 1) / (16 * P::TB) + 1) >= 2147483648.0)
+    return cudaErrorInvalidConfiguration;
+  decode_kernel<BITS, D, ROWS, F32><<<w, kThreads, P::SMEM, s>>>(a, tiles, q, lens, out, arrived, part);
   return cudaGetLastError();
 }
 
 template <int BITS, bool F32>
 cudaError_t by_shape(const Args& a, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s) {
-  const bool two = rows_tile(a) == 16;
-  if (a.d == 64) return two ? go<BITS, 64, 2, F32>(a, q, lens, out, ws, s) : go<BITS, 64, 1, F32>(a, q, lens, out, ws, s);
-  if (a.d == 128) return two ? go<BITS, 128, 2, F32>(a, q, lens, out, ws, s) : go<BITS, 128, 1, F32>(a, q, lens, out, ws, s);
-  return go<BITS, 256, 1, F32>(a, q, lens, out, ws, s);
+  const int r = rows_tile(a);
+#define LOWRAM_KVQ_ROWS(D)                                         \
+  if (r == 4) return go<BITS, D, 4, F32>(a, q, lens, out, ws, s);  \
+  if (r == 8) return go<BITS, D, 8, F32>(a, q, lens, out, ws, s)
+  if (a.d == 64) {
+    LOWRAM_KVQ_ROWS(64);
+    return go<BITS, 64, 16, F32>(a, q, lens, out, ws, s);
+  }
+  if (a.d == 128) {
+    LOWRAM_KVQ_ROWS(128);
+    return go<BITS, 128, 16, F32>(a, q, lens, out, ws, s);
+  }
+  LOWRAM_KVQ_ROWS(256);
+#undef LOWRAM_KVQ_ROWS
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -31,8 +31,9 @@
 //   A of the values:  cell r of tokens 2q, 2q + 1, 2q + 8, 2q + 9 (two tokens' words are merged, then
 //                     masked); code pair (2j, 2j + 1) gives rows r, r + 8 of product j;
 //   outputs C:        channels 64 g + 8 r + 2j (+ 1) x columns 2q, 2q + 1.
-// With at most 4 rows, row j is column 2j and the odd columns are left alone: a lane then holds
-// one row instead of two, and everything that is done per score and per output is halved.
+// With at most 4 rows, row j is column 2j: a lane then holds one row instead of two, and everything
+// that is done per score and per output is halved.  The odd columns take the second part of an
+// fp32 q, and the weights of the next group of channels.
 #pragma once
 
 #include "kvq.cuh"
@@ -129,12 +130,14 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   static constexpr int CP = ROWS == 4 ? 1 : 2;        // rows a lane holds of an 8-column tile
   static constexpr int NT = ROWS == 16 ? 2 : 1;       // 8-column tiles
   static constexpr int G = D / kGroup, ROW = D * BITS / 8;
-  static constexpr int SP = F32 ? 2 : 1;              // fp16 parts of q and of w
+  static constexpr int SP = F32 ? 2 : 1;              // fp16 parts of w
+  static constexpr int SPQ = F32 && CP == 2 ? 2 : 1;  // and of q (CP = 1: the second part is in the odd column)
   static constexpr int STEPS = 4 * G;                 // products of a score tile
-  static constexpr int BLOCK = 2 * 16 * ROW + 2 * 16 * G * 4;   // bytes of 16 tokens in shared memory
-  static constexpr int QFRAG = STEPS * NT * SP * 32 * 8;        // bytes of the queries' B operands
+  static constexpr int CODE = 16 * ROW, META = 16 * G * 4;      // bytes of 16 tokens: codes, scales
+  static constexpr int BLOCK = 2 * (CODE + META);
+  static constexpr int QFRAG = STEPS * NT * SPQ * 32 * 8;       // bytes of the queries' B operands
   static constexpr int QMETA = ROWS * (1 + G) * 4;              // f'' and the group sums
-  static constexpr bool QREG = STEPS * NT * SP * 2 <= 16;       // B operands kept in registers
+  static constexpr bool QREG = STEPS * NT * SPQ * 2 <= 16;       // B operands kept in registers
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   // A score may pass the running maximum by a factor of 2^kSlack in its weight, a value scale leave
   // [2^E, 2^(E+1)) by a factor of kWide either way: w <= 2^(kSlack + 1) kWide kBias < 2^16, and what
@@ -152,7 +155,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   float f[NT][CP], mneg[NT][CP], thr[NT][CP];
   float unit_inv;                                     // kBias 2^-E, 0 before the first scale
   uint32_t top_s;                                     // the largest scale that needs no new unit (fp16 bits)
-  uint2 qr[QREG ? STEPS * NT * SP : 1];
+  uint2 qr[QREG ? STEPS * NT * SPQ : 1];
 
   // The query row of this lane's column (t, c).
   static __device__ __forceinline__ int row_of(int t, int c) {
@@ -215,10 +218,10 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
           float y = x[i] * sigma;
           if (BITS == 4 && reg) y *= 0.0625f;
           const int step = (g * 2 + w % 2) * 2 + half;
-          __half* at = reinterpret_cast<__half*>(frag) + ((((step * NT + tile) * SP) * 32 + col * 4 + w / 2) * 2 + reg) * 2 + hi;
+          __half* at = reinterpret_cast<__half*>(frag) + ((((step * NT + tile) * SPQ) * 32 + col * 4 + w / 2) * 2 + reg) * 2 + hi;
           const __half h = __float2half_rn(y);
           at[0] = h;
-          if constexpr (F32) at[32 * 4] = __float2half_rn(y - __half2float(h));
+          if constexpr (F32) at[CP == 1 ? 4 * 4 : 32 * 4] = __float2half_rn(y - __half2float(h));   // the next column, or the next operand
         }
       }
     }
@@ -227,7 +230,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
     const int lane = threadIdx.x & 31;
     if constexpr (QREG) {
 #pragma unroll
-      for (int i = 0; i < STEPS * NT * SP; ++i) qr[i] = reinterpret_cast<const uint2*>(frag)[i * 32 + lane];
+      for (int i = 0; i < STEPS * NT * SPQ; ++i) qr[i] = reinterpret_cast<const uint2*>(frag)[i * 32 + lane];
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -255,41 +258,50 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   }
 
   // ---------------------------------------------------------------- loading
-  // Starts the copies of 16 tokens, the first at row `row` of the pool.
-  static __device__ __forceinline__ void load(const Args& a, uint32_t dst, size_t row) {
+  // A slot of shared memory holds TB blocks of 16 tokens: [TB] K codes, [TB] V codes, [TB] K scales,
+  // [TB] V scales.
+  // Starts the copies of N blocks whose tokens follow one another from row `row` on, into the slot's
+  // blocks b0, b0 + 1, ...
+  template <int TB, int N> static __device__ __forceinline__ void load(const Args& a, uint32_t slot, int b0, uint32_t row) {
     const int lane = threadIdx.x & 31;
-    constexpr int CODE = 16 * ROW, META = 16 * G * 4;
-    const size_t at = row * ROW + lane * 16;
+    const uint64_t at = (uint64_t)row * ROW + lane * 16;
+    const uint8_t *k = a.k_code + at, *v = a.v_code + at;
+    const uint32_t dst = slot + b0 * CODE + lane * 16;
 #pragma unroll
-    for (int i = 0; i < CODE / 512; ++i) {
-      cp16(dst + i * 512 + lane * 16, a.k_code + at + i * 512);
-      cp16(dst + CODE + i * 512 + lane * 16, a.v_code + at + i * 512);
+    for (int i = 0; i < N * CODE / 512; ++i) {
+      cp16(dst + i * 512, k + i * 512);
+      cp16(dst + TB * CODE + i * 512, v + i * 512);
     }
-    constexpr int MP = META / 16;   // 16-byte pieces of the scales: 4, 8 or 16
-    if (lane < 2 * MP) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(lane < MP ? a.k_scale : a.v_scale);
-      cp16(dst + 2 * CODE + lane * 16, src + row * (G * 4) + (lane % MP) * 16);
+    // the scales of K and V, half of the lanes each
+    constexpr int PIECES = N * META / 16;
+#pragma unroll
+    for (int i = 0; i < (2 * PIECES + 31) / 32; ++i) {
+      const int p = i * 32 + lane, mine = p % PIECES;
+      const bool is_v = p >= PIECES;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? a.v_scale : a.k_scale) + (uint64_t)row * (G * 4) + mine * 16;
+      if (2 * PIECES % 32 == 0 || p < 2 * PIECES) cp16(slot + TB * (2 * CODE + (is_v ? META : 0)) + b0 * META + mine * 16, src);
     }
   }
 
   // ---------------------------------------------------------------- 16 TB tokens
-  // Token t of block i has place tok + 16 i + t; column (t, c) sees the places below lim[t][c].
-  // EDGE: some place is masked; what such a place holds (anything, NaN too) plays no part.
-  template <int TB, bool EDGE>
-  __device__ __forceinline__ void step(const uint8_t* slot, const uint8_t* frag, int tok, const int (&lim)[NT][CP]) {
+  // The slot's blocks b0 .. b0 + N - 1.  Token t of the first has place tok + t; column (t, c) sees the
+  // places below lim[t][c].  EDGE: some place is masked; what such a place holds (anything, NaN too)
+  // plays no part.
+  template <int TB, int N, bool EDGE>
+  __device__ __forceinline__ void step(const uint8_t* slot, int b0, const uint8_t* frag, int tok, const int (&lim)[NT][CP]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-    constexpr int CODE = 16 * ROW, META = 16 * G * 4, CW = BITS / 4;
-    float x[TB][NT][2 * CP];
+    constexpr int CW = BITS / 4;
+    const uint8_t *kc = slot + b0 * CODE, *vc = kc + TB * CODE, *km = slot + TB * 2 * CODE + b0 * META, *vmeta = km + TB * META;
+    float x[N][NT][2 * CP];
     // scores, in units of 1 / f''
 #pragma unroll
-    for (int b = 0; b < TB; ++b) {
-      const uint8_t* base = slot + b * BLOCK;
+    for (int b = 0; b < N; ++b) {
       uint32_t k0[2 * G * CW], k1[2 * G * CW];
-      lds<2 * G * BITS>(k0, base + r * ROW + q * 2 * G * BITS);
-      lds<2 * G * BITS>(k1, base + (r + 8) * ROW + q * 2 * G * BITS);
+      lds<2 * G * BITS>(k0, kc + b * CODE + r * ROW + q * 2 * G * BITS);
+      lds<2 * G * BITS>(k1, kc + b * CODE + (r + 8) * ROW + q * 2 * G * BITS);
       uint32_t m0[G], m1[G];
-      lds<4 * G>(m0, base + 2 * CODE + r * 4 * G);
-      lds<4 * G>(m1, base + 2 * CODE + (r + 8) * 4 * G);
+      lds<4 * G>(m0, km + b * META + r * 4 * G);
+      lds<4 * G>(m1, km + b * META + (r + 8) * 4 * G);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -311,8 +323,12 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int s = 0; s < SP; ++s) mma_f16(acc[t], a0, a1, a2, a3, qop(frag, (((g * 2 + e) * 2 + h) * NT + t) * SP + s));
+              for (int s = 0; s < SPQ; ++s) mma_f16(acc[t], a0, a1, a2, a3, qop(frag, (((g * 2 + e) * 2 + h) * NT + t) * SPQ + s));
           }
+        if constexpr (F32 && CP == 1) {   // the two parts of q
+          acc[0][0] += acc[0][1];
+          acc[0][2] += acc[0][3];
+        }
         const float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&m0[g]));
         const float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&m1[g]));
 #pragma unroll
@@ -335,12 +351,12 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
       }
     }
     // value scales and offsets of the tokens r, r + 8
-    uint32_t vm[TB][2][G], most_s = 0;   // (s, lo) pairs; the largest s in the low half (s >= 0, so its bits are ordered)
+    uint32_t vm[N][2][G], most_s = 0;   // (s, lo) pairs; the largest s in the low half (s >= 0, so its bits are ordered)
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+    for (int b = 0; b < N; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        lds<4 * G>(vm[b][i], slot + b * BLOCK + 2 * CODE + META + (r + 8 * i) * 4 * G);
+        lds<4 * G>(vm[b][i], vmeta + b * META + (r + 8 * i) * 4 * G);
         if constexpr (EDGE) {
           int most = lim[0][0];
 #pragma unroll
@@ -351,20 +367,22 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
             for (int g = 0; g < G; ++g) vm[b][i][g] = 0;
         }
+        if constexpr (G == 1) most_s = __vmaxu2(most_s, vm[b][i][0]);
+        else
 #pragma unroll
-        for (int g = 0; g < G; ++g) most_s = __vmaxu2(most_s, vm[b][i][g]);
+          for (int g = 0; g < G; g += 2) most_s = __vimax3_u16x2(most_s, vm[b][i][g], vm[b][i][g + 1]);
       }
     bool high = (most_s & 0xffffu) > top_s;
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+    for (int b = 0; b < N; ++b)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < 2 * CP; ++k) high |= x[b][t][k] > thr[t][k % CP];
-    if (__any_sync(kFull, high)) move<TB>(x, most_s & 0xffffu);
+    if (__any_sync(kFull, high)) move<N>(x, most_s & 0xffffu);
     // weights: p in x's place, the sum of the weights
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+    for (int b = 0; b < N; ++b)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -373,42 +391,50 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
           x[b][t][k] = p;
           l[t][k % CP] += p;
         }
-    uint32_t v[TB][4][G * CW];   // cell r of the tokens 2q, 2q + 1, 2q + 8, 2q + 9
+    uint32_t v[N][4][G * CW];   // cell r of the tokens 2q, 2q + 1, 2q + 8, 2q + 9
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+    for (int b = 0; b < N; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lds<G * BITS>(v[b][i], slot + b * BLOCK + CODE + (2 * q + (i & 1) + (i >> 1) * 8) * ROW + r * G * BITS);
+      for (int i = 0; i < 4; ++i) lds<G * BITS>(v[b][i], vc + b * CODE + (2 * q + (i & 1) + (i >> 1) * 8) * ROW + r * G * BITS);
+    // The two columns e of a lane are its two rows (CP = 2), or its one row for two groups (CP = 1):
+    // then one operand of weights serves both groups, each taking its own columns of the product.
+    constexpr int SETS = CP == 2 ? G : (G + 1) / 2;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      uint2 w[TB][NT][SP];
+    for (int gs = 0; gs < SETS; ++gs) {
+      uint2 w[N][NT][SP];
       float base[NT][4];   // -kMid sum_t w_t in every row: the products below then add w (n - kMid)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) base[t][k] = 0.f;
 #pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        float2 u[2];
+      for (int b = 0; b < N; ++b) {
+        float2 u[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][i][g]));
-          u[i] = make_float2(m.x * unit_inv, fmaf(kMid, m.x, m.y));
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < (CP == 1 && G > 1 ? 2 : 1); ++e) {
+            const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][i][CP == 2 ? gs : 2 * gs + e]));
+            u[i][e] = make_float2(m.x * unit_inv, fmaf(kMid, m.x, m.y));
+          }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float y[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int c = 0; c < CP; ++c) {
+            for (int e = 0; e < 2; ++e) {
+              const int c = CP == 2 ? e : 0, g = CP == 2 ? gs : 2 * gs + e;
+              if (g >= G) continue;
+              const float2 ue = u[i][CP == 2 ? 0 : e];
               const float p = x[b][t][i * CP + c];
-              y[i][c] = p * u[i].x;
+              y[i][e] = p * ue.x;
               if constexpr (EDGE) {   // a place this column does not see may hold anything
                 const bool seen = tok + 16 * b + r + 8 * i < lim[t][c];
-                y[i][c] = seen ? y[i][c] : 0.f;
-                ls[t][g][c] += seen ? p * u[i].y : 0.f;
+                y[i][e] = seen ? y[i][e] : 0.f;
+                ls[t][g][c] += seen ? p * ue.y : 0.f;
               } else {
-                ls[t][g][c] = fmaf(p, u[i].y, ls[t][g][c]);
+                ls[t][g][c] = fmaf(p, ue.y, ls[t][g][c]);
               }
             }
           if constexpr (F32) {
@@ -425,28 +451,33 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float acc[NT][4];
+      for (int ge = 0; ge < (CP == 1 ? 2 : 1); ++ge) {
+        const int g = CP == 2 ? gs : 2 * gs + ge;
+        if (g >= G) continue;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[t][k] = base[t][k];
-#pragma unroll
-        for (int b = 0; b < TB; ++b) {
-          uint32_t a0, a1, a2, a3;
-          pair_cell<BITS>(v[b][0] + g * CW, v[b][1] + g * CW, j, a0, a1);
-          pair_cell<BITS>(v[b][2] + g * CW, v[b][3] + g * CW, j, a2, a3);
+        for (int j = 0; j < 4; ++j) {
+          float acc[NT][4];
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = SP - 1; i >= 0; --i) mma_f16(acc[t], a0, a1, a2, a3, w[b][t][i]);
+            for (int k = 0; k < 4; ++k) acc[t][k] = base[t][k];
+#pragma unroll
+          for (int b = 0; b < N; ++b) {
+            uint32_t a0, a1, a2, a3;
+            pair_cell<BITS>(v[b][0] + g * CW, v[b][1] + g * CW, j, a0, a1);
+            pair_cell<BITS>(v[b][2] + g * CW, v[b][3] + g * CW, j, a2, a3);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = SP - 1; i >= 0; --i) mma_f16(acc[t], a0, a1, a2, a3, w[b][t][i]);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int c = 0; c < CP; ++c) o[t][g][j][i * CP + c] += acc[t][2 * i + (CP == 2 ? c : ge)];
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < CP; ++c) o[t][g][j][i * CP + c] += acc[t][2 * i + c];
       }
     }
   }

@@ -229,12 +229,13 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   unsigned xa = s0 + warp;                      // the next step to load
   uint8_t* ring = sm + warp * P::STAGES * P::SLOT;
   const uint32_t ring_u = smem_u32(ring);
-  unsigned have = 0;                            // TB bits per step in flight: blocks that are there
-  int pending = 0, in = 0, rd = 0;
-  // Loads run two calls behind the walk: lookup() asks the table for the pages of the next step,
-  // issue() starts the copies of the step looked up before and looks up the one after it.
+  unsigned bad = 0;                             // TB bits per step under way: blocks that are not there
+  int in = 0, rd = 0;
+  // lookup() asks the table for the pages of the next step, issue() starts the copies of the step
+  // looked up before and looks up the one after it.  Rows of the pool are counted in 32 bits (the
+  // host checks; 2^32 rows of 64 channels in 4 bits, K and V, would be 309 GB).
   int seen_b = -1, seen_u = -1, len_a = 0, tok_a = -1, pid_a[TB];
-  size_t unit_row = 0, row_a = 0;               // rows in front of (layer, page 0, head)
+  uint32_t unit_row = 0, row_a = 0;             // rows in front of (layer, page 0, head)
   auto lookup = [&]() {
     tok_a = -1;
     if (xa >= s1) return;
@@ -243,39 +244,42 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       seen_u = ahead.u;
       const int lh = ahead.u / row_tiles, layer = lh / a.Hkv;
       len_a = len_of(a, lens, ahead.b);
-      unit_row = row0_of(a, a.layer0 + layer, 0, lh - layer * a.Hkv);
+      unit_row = (uint32_t)row0_of(a, a.layer0 + layer, 0, lh - layer * a.Hkv);
     }
     row_a = unit_row;
     tok_a = ahead.st * Line<P>::TOK;
 #pragma unroll
-    for (int i = 0; i < TB; ++i) {
-      const int tok = tok_a + 16 * i;
-      if (i > 0 && (tok & (a.page - 1))) pid_a[i] = tok < len_a ? pid_a[i - 1] : -2;
-      else pid_a[i] = tok < len_a ? page_of(a, ahead.b, tok >> a.page_log2) : -2;
-    }
+    for (int i = 0; i < TB; ++i) pid_a[i] = -2;
+    if (tok_a < len_a) pid_a[0] = page_of(a, ahead.b, tok_a >> a.page_log2);
+    if (TB == 2 && a.page == 16 && tok_a + 16 < len_a) pid_a[TB - 1] = page_of(a, ahead.b, (tok_a >> 4) + 1);
     xa += kWarps;
-    line.forward(ahead, kWarps);
+    if (ahead.st + kWarps < ahead.n) ahead.st += kWarps;
+    else line.forward(ahead, kWarps);
   };
-  auto issue = [&]() {
+  // `place`: how many steps are under way
+  auto issue = [&](int place) {
     const int tok = tok_a;
     if (tok >= 0) {
       int pid[TB];
 #pragma unroll
       for (int i = 0; i < TB; ++i) pid[i] = pid_a[i];
-      const size_t row = row_a + (tok & (a.page - 1));
+      const uint32_t row = row_a + (tok & (a.page - 1)), dst = ring_u + in * P::SLOT;
       lookup();
+      if (a.page >= 16 * TB) {                  // one run (its second block may lie behind the last token)
+        if (pid[0] >= 0) Tl::template load<TB, TB>(a, dst, 0, row + ((uint32_t)(pid[0] * a.Hkv) << a.page_log2));
+        else bad |= ((1u << TB) - 1) << (place * TB);
+      } else {
 #pragma unroll
-      for (int i = 0; i < TB; ++i) {
-        if (pid[i] >= 0) {
-          // block i of a step lies in the page of block 0, or at the start of its own (page = 16)
-          const size_t at = row + (((size_t)pid[i] * a.Hkv) << a.page_log2) + (a.page > 16 ? 16 * i : 0);
-          Tl::load(a, ring_u + in * P::SLOT + i * Tl::BLOCK, at);
-          have |= 1u << (pending * TB + i);
-        } else if (pid[i] == -1 && lane == 0) {
-          flag(a, KVQ_ERR_PAGE);
+        for (int i = 0; i < TB; ++i) {
+          if (pid[i] >= 0) Tl::template load<TB, 1>(a, dst, i, row + ((uint32_t)(pid[i] * a.Hkv) << a.page_log2));
+          else bad |= 1u << (place * TB + i);
         }
       }
-      ++pending;
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+          if (pid[i] == -1) flag(a, KVQ_ERR_PAGE);
+      }
       in = in + 1 == P::STAGES ? 0 : in + 1;
     }
     cp_commit();
@@ -300,7 +304,7 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       qr.fetch(rows, warp, [&](int j) { return q + row_at(j); });
       if (first) {
 #pragma unroll 1
-        for (int i = 0; i < P::STAGES - 1; ++i) issue();
+        for (int i = 0; i < P::STAGES - 1; ++i) issue(i);
         first = false;
       }
       qr.prepare(frag, meta, warp);
@@ -319,21 +323,20 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
     for (; st < st1; st += kWarps) {
       cp_wait<P::STAGES - 2>();
       __syncwarp();
-      const unsigned there = have & ((1u << TB) - 1);
-      have >>= TB;
-      --pending;
+      const unsigned gone = bad & ((1u << TB) - 1);
+      bad >>= TB;
       const uint8_t* slot = ring + rd * P::SLOT;
       const int tok = st * Line<P>::TOK;
-      if (there == (1u << TB) - 1 && tok + Line<P>::TOK <= least) {
-        tile.template step<TB, false>(slot, frag, tok, lim);
+      if (gone == 0 && tok + Line<P>::TOK <= least) {
+        tile.template step<TB, TB, false>(slot, 0, frag, tok, lim);
       } else {
 #pragma unroll 1
         for (int i = 0; i < TB; ++i)            // nothing to see in a block that is not there
-          if (there >> i & 1) tile.template step<1, true>(slot + i * Tl::BLOCK, frag, tok + 16 * i, lim);
+          if (!(gone >> i & 1) && tok + 16 * i < len) tile.template step<TB, 1, true>(slot, i, frag, tok + 16 * i, lim);
       }
       rd = rd + 1 == P::STAGES ? 0 : rd + 1;
       __syncwarp();
-      issue();
+      issue(P::STAGES - 2);
     }
     // join the warps: common maximum, scaled sums, channels added warp by warp
     tile.reduce();

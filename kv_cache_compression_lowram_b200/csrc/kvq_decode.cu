@@ -2,8 +2,9 @@
 //
 // Bound by HBM: 2 (d bits / 8 + d / 16) bytes per cached token and KV head, read once per 8 or 16
 // query rows.  All steps of all units -- a unit is (sequence, layer, KV head, tile of query rows), a
-// step 16 or 32 of its tokens -- form one line that is cut into equal pieces, one per CTA, so
-// ragged lengths and few long sequences load the SMs evenly without the host knowing a length.
+// step 16 or 32 of its tokens -- form one line that is shared out evenly among the CTAs (one wave of
+// them), so ragged lengths and few long sequences load the SMs alike without the host knowing a
+// length.
 // A CTA's four warps take its steps in turn, each through a ring of its own in shared memory that
 // cp.async fills ahead, across unit borders; at the end of a unit's part they join their sums.
 // A unit that several CTAs share is joined by the one that finishes last, in the order of the
@@ -18,10 +19,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxWorkers = 640;
-#ifndef KVQ_LEAST
-#define KVQ_LEAST 8
-#endif
-constexpr unsigned kLeast = KVQ_LEAST;
+// How the steps are shared out (measured with 8 units of 10 steps, and 8 of 1024):
+// units of at most kWhole steps are never split -- joining parts through memory costs about 4 us, four
+// steps of a warp about as much -- and a part has at least kLeast steps.
+constexpr unsigned kWhole = 16, kLeast = 8, kSpare = 12;
 constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are fewer
 
 template <int BITS, int D, int ROWS, bool F32> struct Plan {
@@ -68,41 +69,27 @@ template <class P> struct Line {
   int U;   // units of a sequence
   static constexpr int TOK = 16 * P::TB;
   __device__ __forceinline__ int steps(int b) const { return max(1, (len_of(a, lens, b) + TOK - 1) / TOK); }
-  // The steps of all units (the same on every lane; below 2^31, the host checks).  Where there are at
-  // most 32 sequences, `scan` is what at() needs: a lane's steps and their running sum.
-  __device__ __forceinline__ unsigned total(uint2& scan) const {
+  static __device__ __forceinline__ unsigned running_sum(unsigned x) {
     const int lane = threadIdx.x & 31;
-    unsigned t = 0;
-    for (int b = lane; b < a.B; b += 32) t += steps(b) * U;
-    unsigned inc = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned y = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += y;
+      const unsigned y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
     }
-    scan = make_uint2(t, inc);
-    return __shfl_sync(kFull, inc, 31);
+    return x;
   }
-  __device__ __forceinline__ Walk at(unsigned x, uint2 scan) const {   // 0 <= x < total
+  // Place x (below the sum of count(b) over all sequences): its sequence and the rest of x.
+  template <class Count> __device__ __forceinline__ int find(unsigned& x, Count count) const {
     const int lane = threadIdx.x & 31;
-    unsigned before = 0, n = scan.x, inc = scan.y;
     for (int b0 = 0;; b0 += 32) {
-      if (a.B > 32) {
-        n = b0 + lane < a.B ? steps(b0 + lane) * U : 0;
-        inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned y = __shfl_up_sync(kFull, inc, o);
-          if (lane >= o) inc += y;
-        }
-      }
-      const unsigned past = __ballot_sync(kFull, before + inc > x);
+      const unsigned n = b0 + lane < a.B ? count(b0 + lane) : 0, inc = running_sum(n);
+      const unsigned past = __ballot_sync(kFull, inc > x);
       if (past) {
         const int w = __ffs(past) - 1;
-        const unsigned in = x - (before + __shfl_sync(kFull, inc - n, w)), nn = __shfl_sync(kFull, n, w) / U, u = in / nn;
-        return Walk{b0 + w, (int)u, (int)(in - u * nn), (int)nn};
+        x -= __shfl_sync(kFull, inc - n, w);
+        return b0 + w;
       }
-      before += __shfl_sync(kFull, inc, 31);
+      x -= __shfl_sync(kFull, inc, 31);
     }
   }
   __device__ __forceinline__ void next_unit(Walk& w) const {
@@ -122,75 +109,66 @@ template <class P> struct Line {
   }
 };
 
-// The parts of a unit (CTAs c_first .. c_last), joined in their order.  The weights of a chunk of
-// parts are computed side by side, then each thread sums four channels over them with its loads in
-// flight together.  wt: [2][kChunk][ROWS] floats; norm: [ROWS] maxima, then [ROWS] sums.
+// The parts of a unit (CTAs c_first .. c_last), joined in their order.  A warp per row finds the
+// weights of a chunk of parts, then each thread sums four channels over them with its loads in
+// flight together.  wt: [kChunk][ROWS] floats; norm: [ROWS] maxima, then [ROWS] sums.
 template <class P, class Store>
 __device__ __forceinline__ void join_parts(const float* part, int c_first, int c_last, int rows, float* wt, float* norm, Store store) {
-  constexpr int ROWS = P::Tl::ROWS, D = P::Tl::D, REC = ROWS * (D + 2), kChunk = P::JOIN / 8 / ROWS;
-  static_assert(2 * ROWS <= kThreads, "rows");
-  const int tid = threadIdx.x, n = c_last - c_first + 1;
+  constexpr int ROWS = P::Tl::ROWS, D = P::Tl::D, REC = ROWS * (D + 2), kChunk = P::JOIN / 4 / ROWS, FLY = 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = c_last - c_first + 1;
   auto at = [&](int i) { return part + (size_t)(2 * (c_first + i) + (i == 0 ? 1 : 0)) * REC; };
-  // the maxima of all parts: kThreads / ROWS threads a row
-  constexpr int PER = kThreads / ROWS;
-  const int jr = tid % ROWS, pr = tid / ROWS;
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int i = pr; i < n; i += PER) m = fmaxf(m, __ldcg(at(i) + ROWS * D + jr));
-  __syncthreads();
-  wt[pr * ROWS + jr] = m;
-  __syncthreads();
-  if (tid < ROWS) {
-    for (int i = 1; i < PER; ++i) m = fmaxf(m, wt[i * ROWS + tid]);
-    norm[tid] = m;
-    norm[ROWS + tid] = 0.f;
-  }
   constexpr int QUADS = ROWS * D / 4, MINE = (QUADS + kThreads - 1) / kThreads;
   float4 v[MINE];
 #pragma unroll
   for (int k = 0; k < MINE; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += kChunk) {
     const int nc = min(kChunk, n - i0);
-    __syncthreads();
-    float* wl = wt + kChunk * ROWS;
-#pragma unroll 4
-    for (int e = tid; e < nc * ROWS; e += kThreads) {
-      const float* p = at(i0 + e / ROWS) + ROWS * D + e % ROWS;
-      const float mj = norm[e % ROWS], mp = __ldcg(p), lp = __ldcg(p + ROWS);
-      wt[e] = mp == -INFINITY ? 0.f : ex2(mp - mj);
-      wl[e] = mp == -INFINITY ? 0.f : lp * wt[e];
+    if (i0) __syncthreads();
+    for (int j = warp; j < rows; j += kWarps) {
+      if (i0 == 0) {
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(at(i) + ROWS * D + j));
+        m = warp_max(m);
+        if (lane == 0) norm[j] = m;
+      }
+      __syncwarp();
+      const float mj = norm[j];
+      float l = 0.f;
+      for (int i = lane; i < nc; i += 32) {
+        const float* p = at(i0 + i) + ROWS * D + j;
+        const float mp = __ldcg(p), lp = __ldcg(p + ROWS), w = mp == -INFINITY ? 0.f : ex2(mp - mj);
+        wt[i * ROWS + j] = w;
+        l += w == 0.f ? 0.f : w * lp;
+      }
+      l = warp_sum(l);
+      if (lane == 0) norm[ROWS + j] = i0 ? norm[ROWS + j] + l : l;
     }
     __syncthreads();
-    if (tid < ROWS) {
-      float l = norm[ROWS + tid];
-      for (int i = 0; i < nc; ++i) l += wl[i * ROWS + tid];
-      norm[ROWS + tid] = l;
-    }
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
       const int e = tid + k * kThreads, j = e / (D / 4);
       if (j >= rows) continue;
-#pragma unroll 8
-      for (int i = 0; i < nc; ++i) {
-        const float4 p = __ldcg(reinterpret_cast<const float4*>(at(i0 + i)) + e);
-        const float w = wt[i * ROWS + j];
-        if (w != 0.f) {
-          v[k].x = fmaf(w, p.x, v[k].x);
-          v[k].y = fmaf(w, p.y, v[k].y);
-          v[k].z = fmaf(w, p.z, v[k].z);
-          v[k].w = fmaf(w, p.w, v[k].w);
+      for (int i = 0; i < nc; i += FLY) {
+        float4 x[FLY];
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) x[f] = __ldcg(reinterpret_cast<const float4*>(at(i0 + min(i + f, nc - 1))) + e);
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) {
+          const float w = i + f < nc ? wt[(i + f) * ROWS + j] : 0.f;
+          if (w != 0.f) {
+            v[k].x = fmaf(w, x[f].x, v[k].x);
+            v[k].y = fmaf(w, x[f].y, v[k].y);
+            v[k].z = fmaf(w, x[f].z, v[k].z);
+            v[k].w = fmaf(w, x[f].w, v[k].w);
+          }
         }
       }
     }
   }
-  __syncthreads();
 #pragma unroll
   for (int k = 0; k < MINE; ++k) {
     const int e = tid + k * kThreads, j = e / (D / 4);
-    if (j >= rows) continue;
-    const float inv = norm[j] == -INFINITY ? 0.f : 1.f / norm[ROWS + j];
-    store(j, e % (D / 4) * 4, norm[j] == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                  : make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv));
+    if (j < rows) store(j, e % (D / 4) * 4, v[k], norm[j], norm[ROWS + j]);
   }
 }
 
@@ -213,20 +191,79 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   T* out = static_cast<T*>(outv);
   const int rows_all = a.n * a.g;
   const Line<P> line{a, lens, a.n_layers * a.Hkv * row_tiles};
-  uint2 scan;
-  const unsigned total = line.total(scan);
-  // a piece of fewer steps than kLeast would be gone before the joining of its parts
-  const unsigned want = (total + kLeast - 1) / kLeast;
-  const int workers = want < gridDim.x ? (int)want : gridDim.x, me = blockIdx.x;
-  if (me >= workers) return;
+  const int me = blockIdx.x;
+  // This CTA's share: `left` steps from `cur` on.  A part of a unit belongs to the CTAs c_first ..
+  // c_last; where a share is cut anywhere on the line these follow from `cut`.
+  unsigned total = 0, longest = 0, left = 0, s0 = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    const unsigned n = line.steps(b);
+    total += n;
+    longest = max(longest, n);
+  }
+  total = __reduce_add_sync(kFull, total) * line.U;
+  longest = __reduce_max_sync(kFull, longest);
+  Walk cur;
+  int c_first = -1, c_last = 0;
+  Cut cut(1, 1);
+  if (longest <= kWhole) {                      // whole units
+    const unsigned units = a.B * line.U, workers = min(units, gridDim.x);
+    if (me >= workers) return;
+    const Cut c(units, workers);
+    const unsigned u0 = c.begin(me);
+    unsigned n = c.begin(me + 1) - u0;
+    cur.b = u0 / line.U;
+    cur.u = u0 - cur.b * line.U;
+    cur.st = 0;
+    cur.n = line.steps(cur.b);
+    unsigned in_b = min(n, line.U - cur.u);
+    left = in_b * cur.n;
+    for (int b = cur.b + 1; n -= in_b; ++b) {
+      in_b = min(n, (unsigned)line.U);
+      left += in_b * line.steps(b);
+    }
+  } else {
+    // Each unit cut into equal parts of about `piece` steps, one part per CTA, if that takes no more
+    // than kSpare steps more than an even share; else the line cut evenly, across units.
+    const unsigned even = max(kLeast, (total + gridDim.x - 1) / gridDim.x);
+    unsigned piece = even, parts = ~0u;
+    auto parts_of = [&](int b) { return ((unsigned)line.steps(b) + piece - 1) / piece; };
+    if (a.B <= 32)
+      for (; piece <= even + kSpare; piece += 1 + piece / 8) {
+        parts = __reduce_add_sync(kFull, lane < a.B ? parts_of(lane) : 0) * line.U;
+        if (parts <= gridDim.x) break;
+      }
+    if (parts <= gridDim.x) {
+      if (me >= parts) return;
+      unsigned x = me;
+      cur.b = line.find(x, [&](int b) { return parts_of(b) * line.U; });
+      cur.n = line.steps(cur.b);
+      const unsigned k = ((unsigned)cur.n + piece - 1) / piece;
+      cur.u = x / k;
+      const unsigned i = x - cur.u * k;
+      const Cut c(cur.n, k);
+      cur.st = c.begin(i);
+      left = c.begin(i + 1) - cur.st;
+      c_first = me - i;
+      c_last = c_first + k - 1;
+    } else {
+      const unsigned workers = min(gridDim.x, (total + kLeast - 1) / kLeast);
+      if (me >= workers) return;
+      cut = Cut(total, workers);
+      s0 = cut.begin(me);
+      left = cut.begin(me + 1) - s0;
+      unsigned x = s0;
+      cur.b = line.find(x, [&](int b) { return (unsigned)line.steps(b) * line.U; });
+      cur.n = line.steps(cur.b);
+      cur.u = x / cur.n;
+      cur.st = x - cur.u * cur.n;
+    }
+  }
   if (me == 0)
     for (int b = tid; b < a.B; b += kThreads)
       if (len_bad(a, lens, b)) flag(a, KVQ_ERR_RANGE);
-  const Cut cut(total, workers);
-  const unsigned s0 = cut.begin(me), s1 = cut.begin(me + 1);
-  Walk cur = line.at(s0, scan), ahead = cur;
+  Walk ahead = cur;
   line.forward(ahead, warp);
-  unsigned xa = s0 + warp;                      // the next step to load
+  unsigned xa = warp;                           // the next step to load
   uint8_t* ring = sm + warp * P::STAGES * P::SLOT;
   const uint32_t ring_u = smem_u32(ring);
   unsigned bad = 0;                             // TB bits per step under way: blocks that are not there
@@ -238,7 +275,7 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   uint32_t unit_row = 0, row_a = 0;             // rows in front of (layer, page 0, head)
   auto lookup = [&]() {
     tok_a = -1;
-    if (xa >= s1) return;
+    if (xa >= left) return;
     if (ahead.b != seen_b || ahead.u != seen_u) {   // another unit
       seen_b = ahead.b;
       seen_u = ahead.u;
@@ -288,9 +325,8 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
 
   Tl tile;
   bool first = true;
-  for (unsigned x = s0; x < s1;) {              // a unit's part at a time
-    const unsigned x1 = min(s1, x + (cur.n - cur.st));
-    const int unit0 = (int)x - cur.st;          // its first step
+  for (unsigned x = 0; x < left;) {             // a unit's part at a time
+    const unsigned part_n = min(left - x, (unsigned)(cur.n - cur.st));
     const int rt = cur.u % row_tiles, lh = cur.u / row_tiles, layer = lh / a.Hkv, h = lh - layer * a.Hkv;
     const int row_base = rt * ROWS, rows = min(ROWS, rows_all - row_base), len = len_of(a, lens, cur.b);
     // row j of the tile: query token (row_base + j) / g, head (row_base + j) % g of the KV head
@@ -317,9 +353,9 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
 #pragma unroll
       for (int c = 0; c < Tl::CP; ++c) lim[t][c] = len - a.n + 1 + (row_base + min(Tl::row_of(t, c), rows - 1)) / a.g;
     const int least = len - a.n + 1 + row_base / a.g;
-    // this warp's steps of the part: x = s0 + warp modulo kWarps
-    int st = cur.st + (int)((warp - (x - s0) % kWarps + kWarps) % kWarps);
-    const int st1 = cur.st + (int)(x1 - x);
+    // this warp's steps of the part: those that are `warp` modulo kWarps in the share
+    int st = cur.st + (warp - x % kWarps + kWarps) % kWarps;
+    const int st1 = cur.st + part_n;
     for (; st < st1; st += kWarps) {
       cp_wait<P::STAGES - 2>();
       __syncwarp();
@@ -338,70 +374,81 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       __syncwarp();
       issue(P::STAGES - 2);
     }
-    // join the warps: common maximum, scaled sums, channels added warp by warp
+    // join the warps: common maximum, scaled sums, channels added in the warps' order
     tile.reduce();
     tile.store_tops(tops + warp * ROWS, tops + (kWarps + warp) * ROWS);
     __syncthreads();
-    tile.store_out(join + warp * ROWS * D, [&](int j) {
+    auto most = [&](int j) {
       float m = tops[j];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) m = fmaxf(m, tops[w * ROWS + j]);
+      return m;
+    };
+    tile.store_out(join + warp * ROWS * D, [&](int j) {
       const float mine = tops[warp * ROWS + j];
-      return mine == -INFINITY ? 0.f : ex2(mine - m);
+      return mine == -INFINITY ? 0.f : ex2(mine - most(j));
     });
-    __syncthreads();
-    const bool starts = unit0 >= (int)s0, whole = starts && unit0 + cur.n <= (int)s1;
-    constexpr int REC = ROWS * (D + 2);         // floats of a part: [ROWS][D], maxima, sums of the weights
-    float* rec = part + (size_t)(2 * me + (starts ? 1 : 0)) * REC;
-    for (int e = tid; e < rows * D; e += kThreads) {
-      const int j = e / D, c = e % D;
-      float m = tops[j], lsum = 0.f, v = 0.f;
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, tops[w * ROWS + j]);
+    if (tid < ROWS) {                           // meta has done its work
+      const float m = most(tid);
+      float l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = tops[w * ROWS + j];
-        if (mw != -INFINITY) lsum = fmaf(tops[(kWarps + w) * ROWS + j], ex2(mw - m), lsum);
-        v += join[(size_t)(w * ROWS + j) * D + c];
+        const float mw = tops[w * ROWS + tid];
+        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], ex2(mw - m), l);
       }
-      if (whole) {
-        out[row_at(j) + c] = from_f<T>(m == -INFINITY ? 0.f : v / lsum);
+      meta[tid] = m;
+      meta[ROWS + tid] = l;
+    }
+    __syncthreads();
+    const bool whole = cur.st == 0 && part_n == cur.n;
+    constexpr int REC = ROWS * (D + 2);         // floats of a part: [ROWS][D], maxima, sums of the weights
+    float* rec = part + (size_t)(2 * me + (cur.st == 0 ? 1 : 0)) * REC;
+    auto finish = [&](int j, int c, float4 v, float m, float l) {
+      T* o = out + row_at(j) + c;
+      const float inv = 1.f / l;
+      v = m == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      if constexpr (F32) {
+        *reinterpret_cast<float4*>(o) = v;
       } else {
-        rec[e] = v;
-        if (c == 0) {
-          rec[ROWS * D + j] = m;
-          rec[ROWS * D + ROWS + j] = lsum;
-        }
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+        *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(h);
       }
+    };
+    for (int e = tid; e < rows * D / 4; e += kThreads) {
+      const int j = e / (D / 4), c = e % (D / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(join + (w * ROWS + j) * D + c);
+        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+      }
+      if (whole) finish(j, c, v, meta[j], meta[ROWS + j]);
+      else *reinterpret_cast<float4*>(rec + 4 * e) = v;
     }
     if (!whole) {
+      if (tid < 2 * ROWS) rec[ROWS * D + tid] = meta[tid];
       // the last CTA of the unit to come joins all parts, in their order
-      const int c_first = cut.piece_of(unit0), c_last = cut.piece_of(unit0 + cur.n - 1);
-      __threadfence();
+      int c0 = c_first, c1 = c_last;
+      if (c0 < 0) {
+        const unsigned unit0 = s0 + x - cur.st;
+        c0 = cut.piece_of(unit0);
+        c1 = cut.piece_of(unit0 + cur.n - 1);
+      }
       __syncthreads();
-      unsigned* cnt = arrived + (size_t)cur.b * line.U + cur.u;
       if (tid == 0) {
-        const int last = atomicAdd(cnt, 1u) == (unsigned)(c_last - c_first);
+        unsigned* cnt = arrived + (size_t)cur.b * line.U + cur.u;
+        __threadfence();                        // the CTA's writes (seen through the barrier) before the count
+        const int last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
         if (last) *cnt = 0;                     // ready for the next call
+        __threadfence();
         *shared_int = last;
       }
       __syncthreads();
-      if (*shared_int) {
-        __threadfence();
-        join_parts<P>(part, c_first, c_last, rows, join, tops, [&](int j, int c, float4 v) {
-          T* o = out + row_at(j) + c;
-          if constexpr (F32) {
-            *reinterpret_cast<float4*>(o) = v;
-          } else {
-            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
-            *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(h);
-          }
-        });
-      }
+      if (*shared_int) join_parts<P>(part, c0, c1, rows, join, meta, finish);
     }
     __syncthreads();                            // the queries' operands and the sums may be written anew
-    x = x1;
-    cur.st += (int)(x1 - cur.st - unit0);
+    x += part_n;
+    cur.st += part_n;
     if (cur.st >= cur.n) line.next_unit(cur);
   }
   cp_wait<0>();

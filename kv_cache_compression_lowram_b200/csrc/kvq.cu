@@ -147,6 +147,7 @@ lowram_status lowram_kvq_decode_attn(const lowram_kvq_config* cfg, const lowram_
   Args a;
   lowram_status st = check_attn(cfg, cache, layer0, n_layers, n_q, q, lens, out, &a);
   if (st != LOWRAM_OK) return st;
+  if (!decode_line_fits(a)) return inval("too much work for one call: split the layers");
   if (!workspace || !aligned16(workspace) || workspace_bytes < decode_workspace_bytes(a))
     return inval("workspace is NULL, not 16-byte aligned or smaller than lowram_kvq_workspace_bytes");
   return done(launch_decode(a, cfg->dtype, q, lens, out, workspace, reinterpret_cast<cudaStream_t>(stream)), "kvq decode");

@@ -59,6 +59,7 @@ cudaError_t launch_write(const Args& a, int dtype, const Rows& k, const Rows& v,
 cudaError_t launch_read(const Args& a, int dtype, const Rows& k, const Rows& v, const int32_t* pos, const int32_t* count,
                         cudaStream_t s);
 size_t decode_workspace_bytes(const Args& a);
+bool decode_line_fits(const Args& a);
 cudaError_t launch_decode(const Args& a, int dtype, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s);
 cudaError_t launch_sparse(const Args& a, int dtype, int top_k, const void* q, const int32_t* lens, void* out, int32_t* sel,
                           cudaStream_t s);

@@ -19,10 +19,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxWorkers = 640;
-// How the steps are shared out (measured with 8 units of 10 steps, and 8 of 1024):
-// units of at most kWhole steps are never split -- joining parts through memory costs about 4 us, four
-// steps of a warp about as much -- and a part has at least kLeast steps.
-constexpr unsigned kWhole = 16, kLeast = 8, kSpare = 12;
+// How the steps are shared out.  Units of at most kWhole steps are never split: joining parts through
+// memory costs about 4 us, four steps of a warp about as much (one sequence of 301 tokens: 15 us in
+// parts of 8 steps, 8 us whole).  A part has at least kLeast steps.  A unit's queries and its
+// joining cost a CTA about as much as kOver steps: on the line every unit is so much longer.
+// (16 ragged sequences, some of a few tokens: 128 us with 0, 68 with 6, 58 with 10 and with 16.)
+constexpr unsigned kWhole = 16, kLeast = 8, kSpare = 12, kOver = 12;
 constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are fewer
 
 template <int BITS, int D, int ROWS, bool F32> struct Plan {
@@ -194,13 +196,13 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   const int me = blockIdx.x;
   // This CTA's share: `left` steps from `cur` on.  A part of a unit belongs to the CTAs c_first ..
   // c_last; where a share is cut anywhere on the line these follow from `cut`.
-  unsigned total = 0, longest = 0, left = 0, s0 = 0;
+  unsigned total = 0, longest = 0, left = 0, base = 0;   // base: the current unit's place on the line
   for (int b = lane; b < a.B; b += 32) {
     const unsigned n = line.steps(b);
     total += n;
     longest = max(longest, n);
   }
-  total = __reduce_add_sync(kFull, total) * line.U;
+  total = (__reduce_add_sync(kFull, total) + a.B * kOver) * line.U;
   longest = __reduce_max_sync(kFull, longest);
   Walk cur;
   int c_first = -1, c_last = 0;
@@ -224,7 +226,7 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   } else {
     // Each unit cut into equal parts of about `piece` steps, one part per CTA, if that takes no more
     // than kSpare steps more than an even share; else the line cut evenly, across units.
-    const unsigned even = max(kLeast, (total + gridDim.x - 1) / gridDim.x);
+    const unsigned even = max(kLeast, (total - a.B * line.U * kOver + gridDim.x - 1) / gridDim.x);
     unsigned piece = even, parts = ~0u;
     auto parts_of = [&](int b) { return ((unsigned)line.steps(b) + piece - 1) / piece; };
     if (a.B <= 32)
@@ -249,13 +251,32 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       const unsigned workers = min(gridDim.x, (total + kLeast - 1) / kLeast);
       if (me >= workers) return;
       cut = Cut(total, workers);
-      s0 = cut.begin(me);
-      left = cut.begin(me + 1) - s0;
-      unsigned x = s0;
-      cur.b = line.find(x, [&](int b) { return (unsigned)line.steps(b) * line.U; });
-      cur.n = line.steps(cur.b);
-      cur.u = x / cur.n;
-      cur.st = x - cur.u * cur.n;
+      auto place = [&](unsigned x) {
+        Walk w;
+        w.b = line.find(x, [&](int b) { return (line.steps(b) + kOver) * line.U; });
+        w.n = line.steps(w.b);
+        w.u = x / (w.n + kOver);
+        w.st = x - w.u * (w.n + kOver);
+        return w;
+      };
+      const unsigned s0 = cut.begin(me);
+      cur = place(s0);
+      base = s0 - cur.st;
+      if (cur.st >= cur.n) {                    // in the room behind a unit's steps
+        base += cur.n + kOver;
+        line.next_unit(cur);
+      }
+      const Walk last = place(cut.begin(me + 1) - 1);
+      const int to = min(last.st + 1, last.n);
+      int mine = 0;
+      if (cur.b == last.b) {
+        mine = (last.u - cur.u) * cur.n + to - cur.st;
+      } else if (cur.b < last.b) {
+        mine = (line.U - cur.u) * cur.n - cur.st + last.u * last.n + to;
+        for (int b = cur.b + 1; b < last.b; ++b) mine += line.U * line.steps(b);
+      }
+      if (mine <= 0) return;
+      left = mine;
     }
   }
   if (me == 0)
@@ -430,9 +451,8 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       // the last CTA of the unit to come joins all parts, in their order
       int c0 = c_first, c1 = c_last;
       if (c0 < 0) {
-        const unsigned unit0 = s0 + x - cur.st;
-        c0 = cut.piece_of(unit0);
-        c1 = cut.piece_of(unit0 + cur.n - 1);
+        c0 = cut.piece_of(base);
+        c1 = cut.piece_of(base + cur.n - 1);
       }
       __syncthreads();
       if (tid == 0) {
@@ -449,7 +469,10 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
     __syncthreads();                            // the queries' operands and the sums may be written anew
     x += part_n;
     cur.st += part_n;
-    if (cur.st >= cur.n) line.next_unit(cur);
+    if (cur.st >= cur.n) {
+      base += cur.n + kOver;
+      line.next_unit(cur);
+    }
   }
   cp_wait<0>();
 }
@@ -484,9 +507,6 @@ cudaError_t go(const Args& a, const void* q, const int32_t* lens, void* out, voi
   float* part = static_cast<float*>(ws);
   unsigned* arrived = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kPartBytes);
   const int tiles = (a.n * a.g + ROWS - 1) / ROWS;
-  // the line of steps is counted in 32 bits
-  if ((double)a.n_layers * a.B * a.Hkv * tiles * ((((double)a.max_pages * a.page) + 16 * P::TB - 1) / (16 * P::TB) + 1) >= 2147483648.0)
-    return cudaErrorInvalidConfiguration;
   decode_kernel<BITS, D, ROWS, F32><<<w, kThreads, P::SMEM, s>>>(a, tiles, q, lens, out, arrived, part);
   return cudaGetLastError();
 }
@@ -511,6 +531,12 @@ cudaError_t by_shape(const Args& a, const void* q, const int32_t* lens, void* ou
 }
 
 }  // namespace
+
+// The line of steps (of at least 16 tokens) is counted in 32 bits.
+bool decode_line_fits(const Args& a) {
+  const int rt = rows_tile(a), tiles = (a.n * a.g + rt - 1) / rt;
+  return (double)a.n_layers * a.B * a.Hkv * tiles * ((double)a.max_pages * a.page / 16 + 1 + kOver) < 2147483648.0;
+}
 
 size_t decode_workspace_bytes(const Args& a) {
   const int rt = rows_tile(a), tiles = (a.n * a.g + rt - 1) / rt;

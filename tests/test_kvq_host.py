@@ -136,6 +136,8 @@ def test_attention_arguments_are_checked():
         for kw in bad:
             assert attn_call(sparse, **kw) == 1, kw
         assert attn_call(sparse, config(head_dim=80)) == 4
+    # 2^31 steps of 16 tokens and more in one call
+    assert attn_call(False, config(batch=2048, layers=64, kv_heads=8, max_pages=16384, n_pages=9, page=16), n_layers=64) == 1
     need = K.lowram_kvq_workspace_bytes(config(), 1, 1)
     for kw in (dict(ws=None), dict(ws=ODD), dict(ws_bytes=need - 1)):
         assert attn_call(False, **kw) == 1

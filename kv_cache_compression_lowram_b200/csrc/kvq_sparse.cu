@@ -4,13 +4,14 @@
 // CTAs, which do all of it together through each other's shared memory:
 //   1. each CTA scores its share of the full pages (mean key . sum of the group's queries, in 64
 //      bits) into its shared memory: 2 d bytes a page, the larger part of what a long context costs;
-//   2. every CTA gathers all scores and finds the same top_k - 1 best pages: one histogram over the
-//      range of the scores leaves a bin that holds the border, whose few members are ranked by
-//      comparison (a bin too large for that is cut again by the bits of its scores);
+//   2. every CTA gathers all scores, rounded to fp32, and finds the same top_k - 1 best pages: one
+//      histogram over the range of the scores leaves a bin that holds the border, whose few members
+//      are ranked by their 64-bit scores (a bin too large for that is cut again);
 //   3. the selected pages' 16-token blocks go round the warps of the cluster, as in the attention
 //      over whole sequences; CTAs join their sums and the cluster joins the CTAs'.
 // No workspace, no second launch, and nothing is written but the outputs.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include "kvq.cuh"
 #include "kvq_attend.cuh"
@@ -39,71 +40,74 @@ template <int BITS, int D, int ROWS, bool F32> struct Plan {
   static constexpr int MINB = ATTEND <= 72 * 1024 ? 3 : (ATTEND <= 108 * 1024 ? 2 : 1);
 };
 
-// Scores as integers of the same order; NaN as -infinity.
-__device__ __forceinline__ unsigned long long key_of(double s) {
-  if (!(s == s)) s = -INFINITY;
-  s += 0.0;   // -0 as 0
+// Scores: NaN counts as -infinity, -0 as 0.
+__device__ __forceinline__ double plain_score(double s) { return s == s ? s + 0.0 : -INFINITY; }
+// Integers in the order of the numbers, and back.
+__device__ __forceinline__ int key_of(float f) {
+  const int b = __float_as_int(f);
+  return b ^ (b < 0 ? 0x7fffffff : 0);
+}
+__device__ __forceinline__ float float_of(int k) { return __int_as_float(k ^ (k < 0 ? 0x7fffffff : 0)); }
+__device__ __forceinline__ long long key_of(double s) {
   const long long b = __double_as_longlong(s);
-  return (unsigned long long)b ^ (b < 0 ? ~0ull : 0x8000000000000000ull);
-}
-__device__ __forceinline__ double score_of(unsigned long long k) {
-  return __longlong_as_double((long long)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
-}
-
-__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long y = __shfl_xor_sync(kFull, v, o);
-    v = y > v ? y : v;
-  }
-  return v;
+  return b ^ (b < 0 ? 0x7fffffffffffffffll : 0);
 }
 
 struct Select {   // shared by the CTA while it selects
   unsigned hist[kBins];
-  unsigned long long wide[2][kWarps];
+  int wide[2][kWarps];
   unsigned sums[kWarps];
   int border, above, members, list[kRank];
+  double score[kRank];
 };
 
-// Marks (bits of `mark`, zeroed here) the `want` largest of keys[0, n), 0 < want < n; equal ones from the
-// lowest index on.  All threads of the CTA.
-__device__ void select_largest(const unsigned long long* keys, int n, int want, unsigned* mark, Select& s) {
+// How many of the keys of threads 0 .. this one are counted in `x`, this one included.
+__device__ __forceinline__ unsigned scan_cta(unsigned x, unsigned* sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) x += sums[w];
+  return x;
+}
+
+// Marks (bits of `mark`, zeroed here) the `want` largest of n scores, 0 < want < n; equal ones from the
+// lowest index on.  keys[i]: score i rounded to fp32, as key_of(); exact(i): score i; mn, mx: this
+// thread's smallest and largest key of all.  All threads of the CTA.
+template <class Exact>
+__device__ __forceinline__ void select_largest(const int* keys, int n, int want, int mn, int mx, unsigned* mark, Select& s, Exact exact) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < (n + 31) / 32; i += kThreads) mark[i] = 0;
-  unsigned long long lo = 0, hi = ~0ull;   // the keys still in question
+  int lo = INT_MIN, hi = INT_MAX;        // the keys still in question
   bool linear = true;
   for (;;) {
-    // their range
-    unsigned long long mx = 0, mn = 0;     // the largest key, and the largest complement
-    for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long k = keys[i];
-      if (k >= lo && k <= hi) {
-        mx = k > mx ? k : mx;
-        mn = ~k > mn ? ~k : mn;
-      }
-    }
-    mx = warp_max_u64(mx);
-    mn = warp_max_u64(mn);
+    mx = __reduce_max_sync(kFull, mx);
+    mn = __reduce_min_sync(kFull, mn);
     if (lane == 0) {
       s.wide[0][warp] = mx;
       s.wide[1][warp] = mn;
     }
     for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+    if (tid == 0) s.members = 0;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      mx = s.wide[0][w] > mx ? s.wide[0][w] : mx;
-      mn = s.wide[1][w] > mn ? s.wide[1][w] : mn;
+      mx = max(mx, s.wide[0][w]);
+      mn = min(mn, s.wide[1][w]);
     }
-    mn = ~mn;
-    // bins: even in the scores at first (in the keys where a score is infinite), then even in the keys
-    const double smin = score_of(mn), span = score_of(mx) - smin, scale = (kBins - 1) / span;
-    linear = linear && span > 0.0 && span < 1e300 && scale < 1e300;
-    const int shift = mx == mn ? 0 : max(0, 64 - __clzll((long long)(mx - mn)) - 10);
-    auto bin_of = [&](unsigned long long k) { return linear ? (int)((score_of(k) - smin) * scale) : (int)((k - mn) >> shift); };
+    // bins: even in the scores at first (unless one is infinite), then even in the keys
+    const float smin = float_of(mn), span = float_of(mx) - smin, scale = (kBins - 1) / span;
+    linear = linear && span > 0.f && span < 1e38f && scale < 1e38f;
+    const unsigned width = (unsigned)mx - (unsigned)mn;
+    const int shift = max(0, 22 - __clz((int)width));
+    auto bin_of = [&](int k) { return linear ? min((int)((float_of(k) - smin) * scale), kBins - 1) : (int)(((unsigned)k - (unsigned)mn) >> shift); };
+#pragma unroll 4
     for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long k = keys[i];
+      const int k = keys[i];
       if (k >= lo && k <= hi) atomicAdd(&s.hist[bin_of(k)], 1u);
     }
     __syncthreads();
@@ -112,15 +116,7 @@ __device__ void select_largest(const unsigned long long* keys, int n, int want, 
     unsigned sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) sum += s.hist[kBins - 1 - tid * PER - i];
-    unsigned inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned y = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s.sums[warp] = inc;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) inc += s.sums[w];
+    const unsigned inc = scan_cta(sum, s.sums);
     unsigned before = inc - sum;
     if (before < (unsigned)want && inc >= (unsigned)want) {   // one thread
 #pragma unroll
@@ -130,103 +126,130 @@ __device__ void select_largest(const unsigned long long* keys, int n, int want, 
         if (before < (unsigned)want && before + h >= (unsigned)want) {
           s.border = b;
           s.above = before;
-          s.members = h;
         }
         before += h;
       }
     }
     __syncthreads();
-    const int border = s.border, members = s.members;
+    const int border = s.border, inside = s.hist[border];
     want -= s.above;
-    const bool rank = members <= kRank, equal = mx == mn;
-    __syncthreads();
-    if (tid == 0) s.members = 0;
-    __syncthreads();
-    unsigned long long nlo = ~0ull, nhi = 0;
+    const bool rank = inside <= kRank, equal = mx == mn;
+    int nlo = INT_MAX, nhi = INT_MIN;
+#pragma unroll 4
     for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long k = keys[i];
+      const int k = keys[i];
       if (!(k >= lo && k <= hi)) continue;
       const int b = bin_of(k);
       if (b > border) atomicOr(&mark[i >> 5], 1u << (i & 31));
       else if (b == border) {
-        if (rank) s.list[atomicAdd(&s.members, 1)] = i;
-        nlo = k < nlo ? k : nlo;
-        nhi = k > nhi ? k : nhi;
+        if (rank) {
+          const int at = atomicAdd(&s.members, 1);
+          s.list[at] = i;
+          s.score[at] = exact(i);
+        }
+        nlo = min(nlo, k);
+        nhi = max(nhi, k);
       }
     }
+    __syncthreads();
     if (rank) {
-      __syncthreads();
-      for (int j = tid; j < members; j += kThreads) {
+      for (int j = tid; j < inside; j += kThreads) {
         const int i = s.list[j];
-        const unsigned long long k = keys[i];
+        const double x = s.score[j];
         int r = 0;
-        for (int t = 0; t < members; ++t) {
-          const int o = s.list[t];
-          const unsigned long long ko = keys[o];
-          r += ko > k || (ko == k && o < i);
-        }
+        for (int t = 0; t < inside; ++t) r += s.score[t] > x || (s.score[t] == x && s.list[t] < i);
         if (r < want) atomicOr(&mark[i >> 5], 1u << (i & 31));
       }
       __syncthreads();
       return;
     }
-    if (equal) {                                // a run of equal keys: the first `want` of them
-      __syncthreads();
-      if (warp == 0) {
-        int left = want;
-        for (int i = 0; i < n && left > 0; i += 32) {
-          const bool is = i + lane < n && keys[i + lane] == mx;
-          const unsigned m = __ballot_sync(kFull, is);
-          if (is && __popc(m & ((1u << lane) - 1)) < left) atomicOr(&mark[(i + lane) >> 5], 1u << lane);
-          left -= __popc(m);
-        }
-      }
-      __syncthreads();
-      return;
-    }
-    // the border bin alone, by its keys
-    nhi = warp_max_u64(nhi);
-    nlo = warp_max_u64(~nlo);
+    if (equal) break;
+    mn = lo = nlo;                         // the border bin alone, by its keys (the CTA's range: next round)
+    mx = hi = nhi;
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
     if (lane == 0) {
-      s.wide[0][warp] = nhi;
-      s.wide[1][warp] = nlo;
+      s.wide[0][warp] = hi;
+      s.wide[1][warp] = lo;
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      nhi = s.wide[0][w] > nhi ? s.wide[0][w] : nhi;
-      nlo = s.wide[1][w] > nlo ? s.wide[1][w] : nlo;
+      hi = max(hi, s.wide[0][w]);
+      lo = min(lo, s.wide[1][w]);
     }
-    lo = ~nlo;
-    hi = nhi;
     linear = false;
     __syncthreads();
   }
+  // More than kRank scores are one fp32 number: the want-th largest of them, bit by bit from the top of
+  // their 64-bit keys, then the equal ones from the lowest index on.
+  const int same = mx;
+  auto bits = [&](int i) { return (unsigned long long)key_of(exact(i)) ^ 1ull << 63; };   // 0 the smallest
+  if (tid == 0) s.members = -1;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads)
+    if (keys[i] == same) atomicMax(&s.members, i);
+  __syncthreads();
+  const unsigned long long one = bits(s.members);
+  bool differ = false;                     // mostly they are one 64-bit number too
+  for (int i = tid; i < n; i += kThreads) differ |= keys[i] == same && bits(i) != one;
+  differ = __syncthreads_or(differ);
+  unsigned long long top = differ ? 0 : one;   // the bits so far
+  for (int bit = differ ? 63 : -1; bit >= 0; --bit) {
+    const unsigned long long next = top | 1ull << bit;
+    unsigned c = 0;
+    for (int i = tid; i < n; i += kThreads) c += keys[i] == same && bits(i) >= next;
+    c = __reduce_add_sync(kFull, c);
+    if (lane == 0) s.sums[warp] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) c += s.sums[w];
+    if (c >= (unsigned)want) top = next;
+    __syncthreads();
+  }
+  unsigned over = 0;
+  for (int i = tid; i < n; i += kThreads)
+    if (keys[i] == same && bits(i) > top) {
+      atomicOr(&mark[i >> 5], 1u << (i & 31));
+      ++over;
+    }
+  over = __reduce_add_sync(kFull, over);
+  if (lane == 0) s.sums[warp] = over;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) want -= s.sums[w];
+  if (warp == 0)
+    for (int i = 0; i < n && want > 0; i += 32) {
+      const bool is = i + lane < n && keys[i + lane] == same && bits(i + lane) == top;
+      const unsigned m = __ballot_sync(kFull, is);
+      if (is && __popc(m & ((1u << lane) - 1)) < want) atomicOr(&mark[(i + lane) >> 5], 1u << lane);
+      want -= __popc(m);
+    }
+  __syncthreads();
 }
 
 template <int BITS, int D, int ROWS, bool F32>
 __global__ void __launch_bounds__(kThreads, Plan<BITS, D, ROWS, F32>::MINB)
-sparse_kernel(Args a, int top_k, int key_room, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
+sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
               int32_t* __restrict__ sel) {
   using P = Plan<BITS, D, ROWS, F32>;
   using Tl = typename P::Tl;
   using T = typename Tl::T;
   constexpr int TB = P::TB;
   extern __shared__ __align__(128) uint8_t sm[];
-  // attending: ring, joined sums, the queries' operands; selecting: all keys, marks
+  // attending: ring, joined sums, the queries' operands; selecting: this CTA's scores, everyone's keys
   uint8_t* frag = sm + P::RING + P::JOIN;
   float* join = reinterpret_cast<float*>(sm + P::RING);
-  // (a CTA alone has one array for both: key_room = 0)
-  unsigned long long* mine = reinterpret_cast<unsigned long long*>(sm);             // this CTA's scores: [key_room]
-  unsigned long long* keys = mine + key_room;                                       // everyone's
-  const int body = max(P::ATTEND, key_room * 8 + a.max_pages * 8);
+  double* mine = reinterpret_cast<double*>(sm);                                     // [share]
+  int* keys = reinterpret_cast<int*>(mine + share_room);                            // [max_pages]
+  const int body = max(P::ATTEND, share_room * 8 + (a.max_pages * 4 + 7) / 8 * 8);
   unsigned* mark = reinterpret_cast<unsigned*>(sm + body);                          // [max_pages / 32]
   int* list = reinterpret_cast<int*>(mark + (a.max_pages + 31) / 32);               // [top_k] pages, ascending
   float* meta = reinterpret_cast<float*>(list + top_k);
   float* tops = meta + Tl::QMETA / 4;
   float* norm = tops + 2 * kWarps * ROWS;                                           // [ROWS] maxima, [ROWS] sums
   __shared__ Select s;
-  __shared__ int count;
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -246,9 +269,15 @@ sparse_kernel(Args a, int top_k, int key_room, const void* __restrict__ qv, cons
   if (top_k <= last) {
     // 1. scores of the full pages [c0, c1)
     const int share = (last + CS - 1) / CS, c0 = min(rank * share, last), c1 = min(c0 + share, last);
-    constexpr int LPP = D / 8, PPW = 32 / LPP, FLY = 8;
+    constexpr int LPP = D / 8, PPW = 32 / LPP, FLY = 32 / PPW < 16 ? 32 / PPW : 16, STEP = PPW * FLY;   // 32 or 16 pages
     const int c8 = lane % LPP;
     if (top_k > 1) {
+      auto ask = [&](int base) {
+        int pid = -2;
+        if (lane < STEP && base + lane < c1) pid = page_of(a, b, base + lane);
+        return pid;
+      };
+      int pid = ask(c0 + warp * STEP);
       double qs[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) qs[k] = 0.0;
@@ -261,49 +290,67 @@ sparse_kernel(Args a, int top_k, int key_room, const void* __restrict__ qv, cons
         for (int k = 0; k < 8; ++k) qs[k] += (double)to_f<T>(x[k]);
       }
       const uint32_t row = (uint32_t)(row0_of(a, a.layer0 + layer, 0, h) >> a.page_log2);
-      for (int base = c0 + warp * PPW * FLY; base < c1; base += kWarps * PPW * FLY) {
-        int pid = -1;
-        if (lane < PPW * FLY && base + lane < c1) {
-          pid = page_of(a, b, base + lane);
-          if (pid < 0) flag(a, KVQ_ERR_PAGE);
-        }
+      for (int base = c0 + warp * STEP; base < c1; base += kWarps * STEP) {
+        if (pid == -1) flag(a, KVQ_ERR_PAGE);
         uint4 w[FLY];
-        bool there[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
           const int p = __shfl_sync(kFull, pid, f * PPW + lane / LPP);
-          there[f] = p >= 0;
-          w[f] = make_uint4(0, 0, 0, 0);
+          w[f] = make_uint4(0x7fc07fc0u, 0, 0, 0);   // a page that is not there scores NaN
           if (p >= 0) w[f] = __ldg(reinterpret_cast<const uint4*>(a.k_mean + (size_t)(row + (uint32_t)p * a.Hkv) * D) + c8);
         }
+        pid = ask(base + kWarps * STEP);
+        double x[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
           const uint32_t v[4] = {w[f].x, w[f].y, w[f].z, w[f].w};
-          double x = 0.0;
+          x[f] = 0.0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            x = fma(qs[2 * k], (double)__uint_as_float(v[k] << 16), x);
-            x = fma(qs[2 * k + 1], (double)__uint_as_float(v[k] & 0xffff0000u), x);
+            x[f] = fma(qs[2 * k], (double)__uint_as_float(v[k] << 16), x[f]);
+            x[f] = fma(qs[2 * k + 1], (double)__uint_as_float(v[k] & 0xffff0000u), x[f]);
           }
-#pragma unroll
-          for (int o = LPP / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-          const int c = base + f * PPW + lane / LPP;
-          if (c8 == 0 && c < c1) mine[c - c0] = key_of(there[f] ? x : -INFINITY);
         }
+        // sums over the LPP lanes of a page: lanes trade halves of their pages, and with `bits` trades
+        // done a lane holds the pages whose low bits are its own
+        constexpr int TRADES = FLY == 16 ? 4 : 3;
+        int have = FLY;
+#pragma unroll
+        for (int t = 0; t < TRADES; ++t) {
+          have >>= 1;
+          const int o = 1 << t;
+          const bool up = lane & o;
+#pragma unroll
+          for (int f = 0; f < FLY / 2; ++f)
+            if (f < have) {
+              const double keep = up ? x[f + have] : x[f], give = up ? x[f] : x[f + have];
+              x[f] = keep + __shfl_xor_sync(kFull, give, o);
+            }
+        }
+#pragma unroll
+        for (int o = 1 << TRADES; o < LPP; o <<= 1) x[0] += __shfl_xor_sync(kFull, x[0], o);
+        // page f of this lane: bit t of the lane chose the half of size FLY >> (t + 1)
+        int f = 0;
+#pragma unroll
+        for (int t = 0; t < TRADES; ++t) f += (lane >> t & 1) * (FLY >> (t + 1));
+        const int c = base + f * PPW + lane / LPP;
+        if (c8 < (1 << TRADES) && c < c1) mine[c - c0] = plain_score(x[0]);
       }
       // 2. everyone's scores, and the best of them
-      if (CS > 1) {
-        cluster.sync();
-        for (int r = 0; r < CS; ++r) {
-          const unsigned long long* from = cluster.map_shared_rank(mine, r);
-          const int f0 = min(r * share, last), f1 = min(f0 + share, last);
-          for (int c = f0 + tid; c < f1; c += kThreads) keys[c] = from[c - f0];
-        }
-        cluster.sync();                    // `mine` may be overwritten from here on
-      } else {
-        __syncthreads();
+      cluster.sync();
+      int mn = INT_MAX, mx = INT_MIN;
+#pragma unroll 4
+      for (int c = tid; c < last; c += kThreads) {
+        const int r = c / share, k = key_of((float)cluster.map_shared_rank(mine, r)[c - r * share]);
+        keys[c] = k;
+        mn = min(mn, k);
+        mx = max(mx, k);
       }
-      select_largest(keys, last, top_k - 1, mark, s);
+      select_largest(keys, last, top_k - 1, mn, mx, mark, s, [&](int c) {
+        const int r = c / share;
+        return cluster.map_shared_rank(mine, r)[c - r * share];
+      });
+      cluster.sync();                      // `mine` may be overwritten from here on
     } else {
       for (int k = tid; k < (last + 31) / 32; k += kThreads) mark[k] = 0;
       __syncthreads();
@@ -313,17 +360,9 @@ sparse_kernel(Args a, int top_k, int key_room, const void* __restrict__ qv, cons
     int before = 0;
     for (int w0 = 0; w0 < words; w0 += kThreads) {
       const unsigned m = w0 + tid < words ? mark[w0 + tid] : 0;
-      unsigned inc = __popc(m);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) s.sums[warp] = inc;
-      __syncthreads();
-      int at = before + inc - __popc(m);
-      for (int w = 0; w < warp; ++w) at += s.sums[w];
+      int at = before + scan_cta(__popc(m), s.sums) - __popc(m);
       for (unsigned left = m; left; left &= left - 1) list[at++] = (w0 + tid) * 32 + __ffs(left) - 1;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) before += s.sums[w];
       __syncthreads();
     }
@@ -440,20 +479,28 @@ sparse_kernel(Args a, int top_k, int key_room, const void* __restrict__ qv, cons
     }
     // the cluster's CTAs, each joining a part of the outputs
     cluster.sync();
-    for (int e = rank * kThreads + tid; e < rows * D / 4; e += CS * kThreads) {
-      const int j = e / (D / 4);
-      float m = -INFINITY, l = 0.f;
-      for (int r = 0; r < CS; ++r) m = fmaxf(m, cluster.map_shared_rank(norm, r)[j]);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int r = 0; r < CS; ++r) {
-        const float* nr = cluster.map_shared_rank(norm, r);
-        const float mr = nr[j];
-        if (mr == -INFINITY) continue;
-        const float w = ex2(mr - m);
-        l = fmaf(nr[ROWS + j], w, l);
-        const float4 y = reinterpret_cast<const float4*>(cluster.map_shared_rank(join, r))[e];
-        v = make_float4(fmaf(y.x, w, v.x), fmaf(y.y, w, v.y), fmaf(y.z, w, v.z), fmaf(y.w, w, v.w));
+    // CS lanes to four channels, a CTA's part each
+    const int src = tid & (CS - 1);
+    for (int e0 = rank * (kThreads / CS); e0 < rows * D / 4; e0 += kThreads) {
+      const int e = e0 + tid / CS;
+      const bool in = e < rows * D / 4;
+      const int j = in ? e / (D / 4) : 0;
+      const float* nr = cluster.map_shared_rank(norm, src);
+      const float mr = nr[j];
+      float4 v = reinterpret_cast<const float4*>(cluster.map_shared_rank(join, src))[in ? e : 0];
+      float l = nr[ROWS + j], m = mr;
+      for (int o = 1; o < CS; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      const float w = mr == -INFINITY ? 0.f : ex2(mr - m);
+      l = w == 0.f ? 0.f : l * w;
+      v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+      for (int o = 1; o < CS; o <<= 1) {
+        l += __shfl_xor_sync(kFull, l, o);
+        v.x += __shfl_xor_sync(kFull, v.x, o);
+        v.y += __shfl_xor_sync(kFull, v.y, o);
+        v.z += __shfl_xor_sync(kFull, v.z, o);
+        v.w += __shfl_xor_sync(kFull, v.w, o);
       }
+      if (!in || src) continue;
       const float inv = m == -INFINITY ? 0.f : 1.f / l;
       T* o = out + (size_t)row_base * D + 4 * e;
       v = m == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
@@ -471,13 +518,12 @@ sparse_kernel(Args a, int top_k, int key_room, const void* __restrict__ qv, cons
 template <int BITS, int D, int ROWS, bool F32>
 cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, void* out, int32_t* sel, cudaStream_t s) {
   using P = Plan<BITS, D, ROWS, F32>;
-  static int cap[64] = {0};   // per device: the largest cluster, once the attributes are set
+  static int fits[64][5] = {{0}};   // per device: clusters of 1, 2, 4, 8, 16 CTAs resident at once, plus one
   auto kernel = sparse_kernel<BITS, D, ROWS, F32>;
   const unsigned units = (unsigned)a.n_layers * a.B * a.n * a.Hkv;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int most = dev < 64 ? cap[dev] : 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -485,34 +531,43 @@ cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, voi
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto key_room = [&](int cs) { return cs > 1 ? (a.max_pages + cs - 1) / cs : 0; };
+  auto share_room = [&](int cs) { return (a.max_pages + cs - 1) / cs; };
   auto smem_of = [&](int cs) {
-    const int scores = (key_room(cs) + a.max_pages) * 8;
+    const int scores = share_room(cs) * 8 + (a.max_pages * 4 + 7) / 8 * 8;
     return (scores > P::ATTEND ? scores : P::ATTEND) + (a.max_pages + 31) / 32 * 4 + top_k * 4 + P::SMALL + 16;
   };
-  if (!most) {
-    int room = 0;
+  int now[5];
+  int* fit = dev < 64 ? fits[dev] : now;
+  if (dev >= 64 || !fit[0]) {
+    int room = 0, found[5];
     if ((e = cudaDeviceGetAttribute(&room, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
-    room -= (int)sizeof(Select) + 1024;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room)) != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room - (int)fa.sharedSizeBytes)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-    cfg.gridDim = 16;
-    cfg.dynamicSmemBytes = room;
-    attr.val.clusterDim.x = 16;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    int fit = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg)) != cudaSuccess) return e;
-    most = fit > 0 ? 16 : 8;
-    if (dev < 64) cap[dev] = most;
+    cfg.dynamicSmemBytes = P::ATTEND + 4096 + P::SMALL;
+    for (int k = 0; k < 5; ++k) {
+      cfg.gridDim = 1 << k;
+      attr.val.clusterDim.x = 1 << k;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      int n = 0;
+      if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+      found[k] = n + 1;
+    }
+    for (int k = 4; k >= 0; --k) fit[k] = found[k];
   }
-  // as many CTAs of a unit as leave all units resident at once
-  int cs = most;
-  while (cs > 1 && units * cs > 296) cs >>= 1;
+  // the largest cluster that leaves all units resident at once
+  int k = 4;
+  while (k > 0 && (int)units > (fit[k] - 1)) --k;
+#ifdef KVQ_CS
+  k = KVQ_CS;
+#endif
+  const int cs = 1 << k;
   cfg.dynamicSmemBytes = smem_of(cs);
   cfg.gridDim = units * cs;
   attr.val.clusterDim.x = cs;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, top_k, key_room(cs), q, lens, out, sel);
+  return cudaLaunchKernelEx(&cfg, kernel, a, top_k, share_room(cs), q, lens, out, sel);
 }
 
 template <int BITS, bool F32>

@@ -701,40 +701,58 @@ def _kvq_cache_struct(c, arrays) -> LowramKvqCacheC:
     return out
 
 
+_KVQ = None
+
+
+def _kvq_torch():
+    """What every call of the quantised cache needs of torch, looked up once: (torch, the current
+    device's index, a device's current stream as an integer)."""
+    global _KVQ
+    if _KVQ is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the public form takes 3 us
+        _KVQ = (torch, torch.cuda.current_device, raw or (lambda i: torch.cuda.current_stream(i).cuda_stream))
+    return _KVQ
+
+
 def _kvq_call(fn, where, device, stream, *args) -> None:
     """Call `fn` with the data's device current, on `stream` or that device's current stream."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+    torch, current, raw = _kvq_torch()
+    index = device.index
+    s = raw(index) if stream is None else _stream(stream)
+    if index == current():
         st = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
             st = fn(*args, s)
     if st:
         _check(st, where)
 
 
 def _kvq_dtype(c):
-    import torch
+    torch = _kvq_torch()[0]
     return torch.float32 if c.dtype == 0 else torch.bfloat16
+
+
+_I64x4 = ctypes.c_int64 * 4
 
 
 def _kvq_rows(c, t, name, n_layers=None, n=None):
     """(pointer, strides) of a [n_layers][B][n][Hkv][d] tensor with contiguous rows."""
-    if t.dim() != 5 or t.shape[1] != c.batch or t.shape[3] != c.n_kv_heads or t.shape[4] != c.head_dim \
-            or (n_layers is not None and t.shape[0] != n_layers) or (n is not None and t.shape[2] != n):
+    shape = t.shape
+    if len(shape) != 5 or shape[1:4:2] != (c.batch, c.n_kv_heads) or shape[4] != c.head_dim \
+            or (n is not None and (shape[0] != n_layers or shape[2] != n)):
         raise ValueError(f"{name} must be [n_layers][batch][tokens][n_kv_heads][head_dim]")
-    if not t.is_cuda or t.dtype != _kvq_dtype(c) or t.stride(4) != 1:
+    s = t.stride()
+    if not t.is_cuda or t.dtype != _kvq_dtype(c) or s[4] != 1:
         raise ValueError(f"{name} must be a CUDA tensor of the cache's dtype with contiguous rows")
-    return t.data_ptr(), (ctypes.c_int64 * 4)(*t.stride()[:4])
+    return t.data_ptr(), _I64x4(s[0], s[1], s[2], s[3])
 
 
 def _kvq_ints(c, t, name, device):
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != c.batch or t.device != device or t.stride(0) != 1:
+    if t.shape != (c.batch,) or t.dtype != _kvq_torch()[0].int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [batch] tensor on the device of the data")
     return t.data_ptr()
 
@@ -759,9 +777,9 @@ def lowram_kvq_write(cfg, arrays, layer0: int, k, v, pos, count=None, stream=Non
     vp, vs = _kvq_rows(c, v, "v", k.shape[0], k.shape[2])
     if v.device != k.device:
         raise ValueError("k and v must be on one device")
-    _kvq_call(lib().lowram_kvq_write, "lowram_kvq_write", k.device, stream, ctypes.byref(c), ctypes.byref(src), int(layer0),
-              int(k.shape[0]), int(k.shape[2]), kp, ks, vp, vs, _kvq_ints(c, pos, "pos", k.device),
-              _kvq_ints(c, count, "count", k.device))
+    dev, shape = k.device, k.shape
+    _kvq_call(lib().lowram_kvq_write, "lowram_kvq_write", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
+              shape[0], shape[2], kp, ks, vp, vs, _kvq_ints(c, pos, "pos", dev), _kvq_ints(c, count, "count", dev))
 
 
 def lowram_kvq_read(cfg, arrays, layer0: int, k_out, v_out, pos, count=None, stream=None) -> None:
@@ -772,19 +790,20 @@ def lowram_kvq_read(cfg, arrays, layer0: int, k_out, v_out, pos, count=None, str
     vp, vs = _kvq_rows(c, v_out, "v_out", k_out.shape[0], k_out.shape[2])
     if v_out.device != k_out.device:
         raise ValueError("k_out and v_out must be on one device")
-    _kvq_call(lib().lowram_kvq_read, "lowram_kvq_read", k_out.device, stream, ctypes.byref(c), ctypes.byref(src), int(layer0),
-              int(k_out.shape[0]), int(k_out.shape[2]), kp, ks, vp, vs, _kvq_ints(c, pos, "pos", k_out.device),
-              _kvq_ints(c, count, "count", k_out.device))
+    dev, shape = k_out.device, k_out.shape
+    _kvq_call(lib().lowram_kvq_read, "lowram_kvq_read", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
+              shape[0], shape[2], kp, ks, vp, vs, _kvq_ints(c, pos, "pos", dev), _kvq_ints(c, count, "count", dev))
 
 
 def _kvq_queries(c, q, out):
-    if q.dim() != 5 or q.shape[1] != c.batch or q.shape[3] != c.n_q_heads or q.shape[4] != c.head_dim:
+    shape = q.shape
+    if len(shape) != 5 or shape[1:4:2] != (c.batch, c.n_q_heads) or shape[4] != c.head_dim:
         raise ValueError("q must be [n_layers][batch][n_q][n_q_heads][head_dim]")
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
+    if out.shape != shape or out.dtype != q.dtype or out.device != q.device:
         raise ValueError("out must be like q")
     if not q.is_cuda or q.dtype != _kvq_dtype(c):
         raise ValueError("q must be a CUDA tensor of the cache's dtype")
-    return _ptr(q), _ptr(out)
+    return _ptr(q), _ptr(out), shape
 
 
 def lowram_kvq_decode_attn(cfg, arrays, layer0: int, q, lens, out, workspace, stream=None) -> None:
@@ -792,12 +811,13 @@ def lowram_kvq_decode_attn(cfg, arrays, layer0: int, q, lens, out, workspace, st
     sequences of lens[b] tokens.  ``workspace``: lowram_kvq_workspace_bytes bytes, zeroed once."""
     c = kvq_config_struct(cfg)
     src = _kvq_cache_struct(c, arrays)
-    qp, op = _kvq_queries(c, q, out)
-    if workspace.device != q.device:
+    qp, op, shape = _kvq_queries(c, q, out)
+    dev = q.device
+    if workspace.device != dev:
         raise ValueError("workspace must be on the device of q")
-    _kvq_call(lib().lowram_kvq_decode_attn, "lowram_kvq_decode_attn", q.device, stream, ctypes.byref(c), ctypes.byref(src),
-              int(layer0), int(q.shape[0]), int(q.shape[2]), qp, _kvq_ints(c, lens, "lens", q.device), op,
-              _ptr(workspace), workspace.numel() * workspace.element_size())
+    _kvq_call(lib().lowram_kvq_decode_attn, "lowram_kvq_decode_attn", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
+              shape[0], shape[2], qp, _kvq_ints(c, lens, "lens", dev), op, _ptr(workspace),
+              workspace.numel() * workspace.element_size())
 
 
 def lowram_kvq_sparse_attn(cfg, arrays, layer0: int, top_k: int, q, lens, out, sel=None, stream=None) -> None:
@@ -805,15 +825,13 @@ def lowram_kvq_sparse_attn(cfg, arrays, layer0: int, top_k: int, q, lens, out, s
     [n_layers][B][n_q][Hkv][top_k] int32 takes their places in the sequence (then -1)."""
     c = kvq_config_struct(cfg)
     src = _kvq_cache_struct(c, arrays)
-    qp, op = _kvq_queries(c, q, out)
-    if sel is not None:
-        import torch
-        if tuple(sel.shape) != tuple(q.shape[:3]) + (c.n_kv_heads, int(top_k)) or sel.dtype != torch.int32 \
-                or sel.device != q.device:
-            raise ValueError("sel must be int32 [n_layers][batch][n_q][n_kv_heads][top_k] on the device of q")
-    _kvq_call(lib().lowram_kvq_sparse_attn, "lowram_kvq_sparse_attn", q.device, stream, ctypes.byref(c), ctypes.byref(src),
-              int(layer0), int(q.shape[0]), int(q.shape[2]), int(top_k), qp, _kvq_ints(c, lens, "lens", q.device), op,
-              _ptr(sel))
+    qp, op, shape = _kvq_queries(c, q, out)
+    dev = q.device
+    if sel is not None and (tuple(sel.shape) != tuple(shape[:3]) + (c.n_kv_heads, top_k)
+                            or sel.dtype != _kvq_torch()[0].int32 or sel.device != dev):
+        raise ValueError("sel must be int32 [n_layers][batch][n_q][n_kv_heads][top_k] on the device of q")
+    _kvq_call(lib().lowram_kvq_sparse_attn, "lowram_kvq_sparse_attn", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
+              shape[0], shape[2], top_k, qp, _kvq_ints(c, lens, "lens", dev), op, _ptr(sel))
 
 
 class LowramKvq:
@@ -856,8 +874,8 @@ class LowramKvq:
              stream=None):
         """(k, v) [n_layers][B][n][Hkv][d] of tokens pos[b] + i; rows behind count[b] are left as
         they are in ``out`` (zero without it)."""
-        import torch
         if out is None:
+            torch = _kvq_torch()[0]
             c = self.config
             shape = (c.n_layers - layer0 if n_layers is None else n_layers, c.batch, n, c.n_kv_heads, c.head_dim)
             out = tuple(torch.zeros(shape, dtype=_kvq_dtype(c), device=self.device) for _ in range(2))
@@ -867,20 +885,19 @@ class LowramKvq:
 
     def decode(self, q, lens, out=None, layer0: int = 0, stream=None):
         """Attention of q [n_layers][B][n_q][Hq][d] over whole sequences of lens[b] tokens."""
-        import torch
         self._mine(q)
         if out is None:
-            out = torch.empty_like(q)
+            out = _kvq_torch()[0].empty_like(q)
         lowram_kvq_decode_attn(self.config, self._cache, layer0, q, lens, out, self._workspace, stream)
         return out
 
     def decode_sparse(self, q, lens, top_k: int, out=None, sel: bool = False, layer0: int = 0, stream=None):
         """The same over each query's newest page and its top_k - 1 best older pages."""
-        import torch
         self._mine(q)
+        torch = _kvq_torch()[0]
         if out is None:
             out = torch.empty_like(q)
-        s = torch.empty(tuple(q.shape[:3]) + (self.config.n_kv_heads, int(top_k)), dtype=torch.int32,
+        s = torch.empty(tuple(q.shape[:3]) + (self.config.n_kv_heads, top_k), dtype=torch.int32,
                         device=q.device) if sel else None
         lowram_kvq_sparse_attn(self.config, self._cache, layer0, top_k, q, lens, out, s, stream)
         return (out, s) if sel else out

@@ -4,17 +4,25 @@
 // d * sizeof(dt) bytes on one side and d * bits / 8 + d / 16 on the other.  A CTA takes the
 // part of one page that a call touches, for one (layer, sequence, KV head): the page's codes
 // and scales are one contiguous block each, the caller's rows are d-long pieces that
-// neighbouring CTAs (the next head) continue.  Half of its warps take K, half V; a lane
-// holds 8 channels (16 bytes of bf16), so 8 lanes hold a group and its minimum and maximum
-// are three shuffles.
+// neighbouring CTAs (the next head) continue.  Half of its warps take K, half V.
+//
+// Writing is limited by instructions as much as by memory, so a lane holds 16 channels (4 lanes a
+// group: the minimum and maximum are two shuffles, of a packed pair for bf16, and what a group
+// costs once is spread over 16 values), and a code is one FFMA and one rounding add, with the
+// distance to the next half step watched beside it: only where a value is too near to one is the
+// remainder computed exactly.
 #include "kvq.cuh"
 
 namespace lowram {
 namespace kvq {
 namespace {
 
+#ifndef KVQ_FLY
+#define KVQ_FLY 2
+#define KVQ_WB 6
+#endif
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;   // rows in flight per lane
+constexpr int kUnroll = 4;   // rows that a lane of the reading kernel has in flight
 constexpr unsigned kAll = 0xffffffffu;
 
 // fp32 value of a small non-negative integer sits in the low mantissa bits of x + kMagic.
@@ -101,62 +109,146 @@ __device__ __forceinline__ void dequant(const Cell<BITS>& c, __half2 meta, float
     x[i] = fmaf(s, __uint_as_float(0x4B000000u | c.code(i)) - 8388608.0f, lo);
 }
 
-// Codes and (s, lo) of the group that this lane's 8 neighbours share.
-template <typename T, int BITS>
-__device__ __forceinline__ void quantise(const float (&x)[8], Cell<BITS>& c, __half2& meta) {
-  constexpr float kQ = (float)((1 << BITS) - 1);
+// Smallest and largest of the group's 64 values, 16 of which this lane holds; NaN if any is.
+__device__ __forceinline__ float2 group_range(const Raw8<float> (&raw)[2]) {
+  float x[16];
+  raw[0].get(*reinterpret_cast<float(*)[8]>(x));
+  raw[1].get(*reinterpret_cast<float(*)[8]>(x + 8));
   float mn = x[0], mx = x[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
+  for (int i = 1; i < 16; ++i) {
     mn = min_nan(mn, x[i]);
     mx = max_nan(mx, x[i]);
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int o = 1; o < 4; o <<= 1) {
     mn = min_nan(mn, __shfl_xor_sync(kAll, mn, o));
     mx = max_nan(mx, __shfl_xor_sync(kAll, mx, o));
   }
-  // bf16 values differ exactly in fp32 unless one is below 2^-16 of the other
-  float sf;
-  if constexpr (sizeof(T) == 2) sf = __fdiv_rn(mx - mn, kQ);
-  else sf = (float)(((double)mx - (double)mn) / (double)kQ);
-  meta = __halves2half2(__float2half_rn(sf), __float2half_rn(mn));
-  const float s = __low2float(meta), lo = __high2float(meta);
-  const bool usable = s > 0.f && s < INFINITY && fabsf(lo) < INFINITY;
-  const float inv = usable ? __frcp_rn(s) : 0.f, off = usable ? -lo * inv : 0.f;
-  // Fast codes: f = x inv + off = (x - lo) / s up to (2 kQ + |off|) 2^-24 (inv, off and the
-  // sum are each off by 2^-24 relative), rounded by adding kMagic.  A value nearer than twice
-  // that to a half step, and a group whose rounded lo or s lets codes leave [0, 2^b - 1], take
-  // the exact path below.
-  const float tie = 0.5f - (2.f * kQ + fabsf(off)) * 1.1920929e-7f;
-  float near = 0.f;
-  uint32_t bits[8];
+  return make_float2(mn, mx);
+}
+__device__ __forceinline__ float2 group_range(const Raw8<__nv_bfloat16> (&raw)[2]) {
+  const uint32_t w[8] = {raw[0].w.x, raw[0].w.y, raw[0].w.z, raw[0].w.w, raw[1].w.x, raw[1].w.y, raw[1].w.z, raw[1].w.w};
+  auto h2 = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+  __nv_bfloat162 mn = h2(w[0]), mx = mn;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = fmaf(x[i], inv, off), r = f + kMagic;
-    bits[i] = __float_as_uint(r);
-    near = fmaxf(near, fabsf(f - (r - kMagic)));
+  for (int i = 1; i < 8; ++i) {
+    mn = __hmin2_nan(mn, h2(w[i]));
+    mx = __hmax2_nan(mx, h2(w[i]));
   }
-  const bool inside = fmaf(mn, inv, off) > -0.49f && fmaf(mx, inv, off) < kQ + 0.49f;
-  if (usable && !(inside && near < tie)) {
+  // one pair (min, -max), so that each further step is one minimum
+  const __nv_bfloat162 ng = __hneg2(mx);
+  __nv_bfloat162 m = __hmin2_nan(__lows2bfloat162(mn, ng), __highs2bfloat162(mn, ng));
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const uint32_t y = __shfl_xor_sync(kAll, *reinterpret_cast<uint32_t*>(&m), o);
+    m = __hmin2_nan(m, h2(y));
+  }
+  return make_float2(__low2float(m), -__high2float(m));
+}
+
+// What the codes of a group are made with.
+struct Scale {
+  float s, lo, inv, off;
+  bool usable, inside;   // not a constant group or one with non-finite values; codes cannot leave [0, 2^b - 1]
+};
+template <typename T, int BITS>
+__device__ __forceinline__ Scale scale_of(float2 range, __half2& meta) {
+  constexpr float kQ = (float)((1 << BITS) - 1), kInvQ = 1.f / kQ;
+  const float mn = range.x, mx = range.y;
+  float sf;
+  if constexpr (sizeof(T) == 2) {
+    // (bf16 values differ exactly in fp32 unless one is below 2^-16 of the other.)  A correctly
+    // rounded quotient by the constant: one step of residual correction.
+    const float span = mx - mn, q = span * kInvQ;
+    sf = fmaf(fmaf(-q, kQ, span), kInvQ, q);
+  } else {
+    sf = (float)(((double)mx - (double)mn) / (double)kQ);
+  }
+  meta = __floats2half2_rn(sf, mn);
+  Scale g;
+  g.s = __low2float(meta);
+  g.lo = __high2float(meta);
+  g.usable = g.s > 0.f && g.s < INFINITY && fabsf(g.lo) < INFINITY;
+  const float inv = __fdividef(1.f, g.s);
+  g.inv = g.usable ? fmaf(inv, fmaf(-g.s, inv, 1.f), inv) : 0.f;
+  g.off = g.usable ? -g.lo * g.inv : 0.f;
+  g.inside = fmaf(mn, g.inv, g.off) > -0.49f && fmaf(mx, g.inv, g.off) < kQ + 0.49f;
+  return g;
+}
+
+// The codes of 8 channels, as a cell and as numbers.
+template <typename T, int BITS>
+__device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cell<BITS>& c, float (&nf)[8]) {
+  constexpr float kQ = (float)((1 << BITS) - 1);
+  float x[8], near = 0.f;
+  uint32_t bits[8];
+  raw.get(x);
+  bool exact = !g.inside;
+  if constexpr (sizeof(T) == 2) {
+    // t = x - lo is exact (but for x below 2^-16 of lo), and so is the remainder e = t - n s: a code
+    // is right where |e| < s / 2.  Values of 8 bits do meet half steps: every 28th group of 64 normal
+    // values has one in 4 bits.
+    const float hs = 0.5f * g.s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      double f = rint(((double)x[i] - (double)lo) / (double)s);
-      f = f < 0.0 ? 0.0 : (f > (double)kQ ? (double)kQ : f);
-      bits[i] = kMagicBits + (uint32_t)(int)f;
+      const float t = x[i] - g.lo, r = fmaf(t, g.inv, kMagic);
+      bits[i] = __float_as_uint(r);
+      nf[i] = r - kMagic;
+      near = fmaxf(near, fabsf(fmaf(-nf[i], g.s, t)));
+    }
+    if (near >= hs) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e = fmaf(-nf[i], g.s, x[i] - g.lo);
+        if (fabsf(e) > hs || (fabsf(e) == hs && (bits[i] & 1u))) {
+          nf[i] += copysignf(1.f, e);
+          bits[i] = __float_as_uint(nf[i] + kMagic);
+        }
+      }
+    }
+  } else {
+    // f = x inv + off = (x - lo) / s up to (2 kQ + |off|) 2^-24 (inv, off and the sum are each off by
+    // 2^-24 relative), rounded by adding kMagic.  A value nearer than twice that to a half step takes
+    // the exact path below.
+    const float tie = 0.5f - (2.f * kQ + fabsf(g.off)) * 1.1920929e-7f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = fmaf(x[i], g.inv, g.off), r = f + kMagic;
+      bits[i] = __float_as_uint(r);
+      nf[i] = r - kMagic;
+      near = fmaxf(near, fabsf(f - nf[i]));
+    }
+    exact |= !(near < tie);
+  }
+  if (exact && g.usable) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // t + te = x - lo exactly; n the nearest code up to one; m = t - n s exactly (n s has 19 bits and
+      // is within s of t); so the sign of 2 (m + te) -+ s is known
+      const float t = x[i] - g.lo, z = t - x[i], te = (x[i] - (t - z)) + (-g.lo - z);
+      float n = fminf(fmaxf(t * g.inv, -1.f), kQ + 1.f);
+      n = (n + kMagic) - kMagic;
+      const float m = fmaf(-n, g.s, t), above = (2.f * m - g.s) + 2.f * te, below = (2.f * m + g.s) + 2.f * te;
+      const bool odd = __float_as_uint(n + kMagic) & 1u;
+      if (above > 0.f || (above == 0.f && odd)) n += 1.f;
+      else if (below < 0.f || (below == 0.f && odd)) n -= 1.f;
+      n = fminf(fmaxf(n, 0.f), kQ);
+      nf[i] = n;
+      bits[i] = __float_as_uint(n + kMagic);
     }
   }
   // sum of code_i << (BITS * i), the magic bits taken off once (arithmetic modulo 2^32)
+  constexpr int kPer = 32 / BITS;
 #pragma unroll
   for (int j = 0; j < BITS / 4; ++j) {
-    constexpr int kPer = 32 / BITS;
     uint32_t w = 0, m = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       w += bits[j * kPer + i] << (BITS * i);
       m += kMagicBits << (BITS * i);
     }
-    c.w[j] = usable ? w - m : 0u;
+    c.w[j] = w - m;
   }
 }
 
@@ -194,9 +286,9 @@ __device__ __forceinline__ bool piece_of(const Args& a, const int32_t* pos, cons
 }
 
 template <typename T, int BITS, int D>
-__global__ void __launch_bounds__(kThreads) write_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
+__global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
                                                          const int32_t* __restrict__ count, int pieces) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 2 * RPW, G = D / kGroup, ROW = D * BITS / 8;
+  constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 2 * RPW, G = D / kGroup, ROW = D * BITS / 8, FLY = KVQ_FLY;
   __shared__ float sums[STEP][D];
   Piece p;
   if (!piece_of(a, pos, count, pieces, &p)) return;
@@ -207,59 +299,70 @@ __global__ void __launch_bounds__(kThreads) write_kernel(Args a, Rows k, Rows v,
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool is_v = warp >= 2;
-  const int rsub = (warp & 1) * RPW + lane / LPR, c8 = lane % LPR, grp = c8 / 8, cell = (c8 % 8) * G + grp;
+  const int rsub = (warp & 1) * RPW + lane / LPR, l16 = lane % LPR, grp = l16 / 4, cell = l16 % 4 * 2 * G + grp;
   const Rows& src = is_v ? v : k;
   const char* in = static_cast<const char*>(src.p) +
-                   sizeof(T) * (p.layer * src.layer + p.b * src.seq + p.h * src.head + c8 * 8);
+                   sizeof(T) * (p.layer * src.layer + p.b * src.seq + p.h * src.head + l16 * 16);
   const size_t row0 = row0_of(a, a.layer0 + p.layer, pid, p.h);
   uint8_t* code = (is_v ? a.v_code : a.k_code) + row0 * ROW + cell * BITS;
   __half2* scale = (is_v ? a.v_scale : a.k_scale) + row0 * G + grp;
   const bool mean = p.s1 == a.page && a.k_mean != nullptr;
-  float acc[8];
+  // Rows of slot t belong to the lanes with rsub = t mod STEP, and a lane sums s n and lo of its rows
+  // in their order, so a page's mean is one sum however its tokens arrived.
+  float acc[16], los = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  // Rows of slot t belong to the lanes with rsub = t mod STEP, so a page's mean is summed in
-  // one order however its tokens arrived.
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   if (mean && !is_v)
     for (int t = rsub; t < p.s0; t += STEP) {
-      Cell<BITS> c;
-      float x[8];
-      c.load(code + (size_t)t * ROW);
-      dequant<BITS>(c, scale[(size_t)t * G], x);
+      Cell<BITS> c[2];
+      c[0].load(code + (size_t)t * ROW);
+      c[1].load(code + (size_t)t * ROW + G * BITS);
+      const __half2 meta = scale[(size_t)t * G];
+      const float s = __low2float(meta);
+      los += __high2float(meta);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += x[i];
+      for (int i = 0; i < 16; ++i) acc[i] = fmaf(s, (float)c[i / 8].code(i % 8), acc[i]);
     }
-  for (int base = p.s0 & ~(STEP - 1); base < p.s1; base += STEP * kUnroll) {
-    Raw8<T> raw[kUnroll];
+  for (int base = p.s0 & ~(STEP - 1); base < p.s1; base += STEP * FLY) {
+    Raw8<T> raw[FLY][2];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < FLY; ++u) {
       const int t = base + u * STEP + rsub;
-      if (t >= p.s0 && t < p.s1) raw[u].load(in + sizeof(T) * ((int64_t)(p.tok0 + t) * src.tok));
-      else raw[u].zero();
+      if (t >= p.s0 && t < p.s1) {
+        const char* at = in + sizeof(T) * ((int64_t)(p.tok0 + t) * src.tok);
+        raw[u][0].load(at);
+        raw[u][1].load(at + 8 * sizeof(T));
+      } else {
+        raw[u][0].zero();
+        raw[u][1].zero();
+      }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < FLY; ++u) {
       const int t = base + u * STEP + rsub;
       if (base + u * STEP >= p.s1) break;
-      float x[8];
-      Cell<BITS> c;
       __half2 meta;
-      raw[u].get(x);
-      quantise<T, BITS>(x, c, meta);
+      const Scale sc = scale_of<T, BITS>(group_range(raw[u]), meta);
       if (t < p.s0 || t >= p.s1) continue;
-      c.store(code + (size_t)t * ROW);
-      if ((c8 & 7) == 0) scale[(size_t)t * G] = meta;
-      if (mean && !is_v) {
-        dequant<BITS>(c, meta, x);
+      if ((l16 & 3) == 0) scale[(size_t)t * G] = meta;
+      los += sc.lo;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += x[i];
+      for (int j = 0; j < 2; ++j) {
+        float nf[8];
+        Cell<BITS> c;
+        codes_of<T, BITS>(raw[u][j], sc, c, nf);
+        c.store(code + (size_t)t * ROW + j * G * BITS);
+        if (mean && !is_v) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[8 * j + i] = fmaf(sc.s, nf[i], acc[8 * j + i]);
+        }
       }
     }
   }
   if (!mean) return;   // the same for the whole CTA
   if (!is_v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[rsub][c8 * 8 + i] = acc[i];
+    for (int i = 0; i < 16; ++i) sums[rsub][l16 * 16 + i] = acc[i] + los;
   }
   __syncthreads();
   __nv_bfloat16* out = a.k_mean + (row0 >> a.page_log2) * D;

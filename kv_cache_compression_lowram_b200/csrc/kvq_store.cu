@@ -6,7 +6,8 @@
 // and scales are one contiguous block each, the caller's rows are d-long pieces that
 // neighbouring CTAs (the next head) continue.  Half of its warps take K, half V.
 //
-// Writing is limited by instructions as much as by memory, so a lane holds 16 channels (4 lanes a
+// Writing is limited by instructions as much as by memory, so numbers go two to a register (channels
+// k and k + 4 of a cell) through the packed fp32 operations, a lane holds 16 channels (4 lanes a
 // group: the minimum and maximum are two shuffles, of a packed pair for bf16, and what a group
 // costs once is spread over 16 values), and a code is one FFMA and one rounding add, with the
 // distance to the next half step watched beside it: only where a value is too near to one is the
@@ -25,9 +26,9 @@ constexpr int kThreads = 128;
 constexpr int kUnroll = 4;   // rows that a lane of the reading kernel has in flight
 constexpr unsigned kAll = 0xffffffffu;
 
-// fp32 value of a small non-negative integer sits in the low mantissa bits of x + kMagic.
+// x + kMagic - kMagic is x rounded to an integer (half to even; |x| < 2^22), whose parity is the last
+// bit of x + kMagic.
 constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
-constexpr uint32_t kMagicBits = 0x4B400000u;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -46,6 +47,11 @@ template <> struct Raw8<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void load(const void* p) { w = __ldcs(static_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  // channels k and k + 4
+  __device__ __forceinline__ F2 pair(int k) const {
+    const uint32_t a = k < 2 ? w.x : w.y, b = k < 2 ? w.z : w.w;
+    return k & 1 ? F2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)) : F2(__uint_as_float(a << 16), __uint_as_float(b << 16));
+  }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -68,6 +74,9 @@ template <> struct Raw8<float> {
     w1 = __ldcs(static_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void zero() { w0 = w1 = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ F2 pair(int k) const {
+    return k == 0 ? F2(w0.x, w1.x) : (k == 1 ? F2(w0.y, w1.y) : (k == 2 ? F2(w0.z, w1.z) : F2(w0.w, w1.w)));
+  }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = w0.x; x[1] = w0.y; x[2] = w0.z; x[3] = w0.w;
     x[4] = w1.x; x[5] = w1.y; x[6] = w1.z; x[7] = w1.w;
@@ -177,34 +186,35 @@ __device__ __forceinline__ Scale scale_of(float2 range, __half2& meta) {
   return g;
 }
 
-// The codes of 8 channels, as a cell and as numbers.
+// The codes of 8 channels, as a cell and as numbers (nf[k]: channels k and k + 4).
 template <typename T, int BITS>
-__device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cell<BITS>& c, float (&nf)[8]) {
+__device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cell<BITS>& c, F2 (&nf)[4]) {
   constexpr float kQ = (float)((1 << BITS) - 1);
-  float x[8], near = 0.f;
-  uint32_t bits[8];
-  raw.get(x);
+  const F2 magic(kMagic), unmagic(-kMagic), inv(g.inv);
+  float near = 0.f;
   bool exact = !g.inside;
   if constexpr (sizeof(T) == 2) {
     // t = x - lo is exact (but for x below 2^-16 of lo), and so is the remainder e = t - n s: a code
     // is right where |e| < s / 2.  Values of 8 bits do meet half steps: every 28th group of 64 normal
     // values has one in 4 bits.
     const float hs = 0.5f * g.s;
+    const F2 minus_lo(-g.lo), minus_s(-g.s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = x[i] - g.lo, r = fmaf(t, g.inv, kMagic);
-      bits[i] = __float_as_uint(r);
-      nf[i] = r - kMagic;
-      near = fmaxf(near, fabsf(fmaf(-nf[i], g.s, t)));
+    for (int k = 0; k < 4; ++k) {
+      const F2 t = add2(raw.pair(k), minus_lo);
+      nf[k] = add2(fma2(t, inv, magic), unmagic);
+      const float2 e = fma2(nf[k], minus_s, t).get();
+      near = fmaxf(near, fmaxf(fabsf(e.x), fabsf(e.y)));
     }
     if (near >= hs) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = fmaf(-nf[i], g.s, x[i] - g.lo);
-        if (fabsf(e) > hs || (fabsf(e) == hs && (bits[i] & 1u))) {
-          nf[i] += copysignf(1.f, e);
-          bits[i] = __float_as_uint(nf[i] + kMagic);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float2 e = fma2(nf[k], minus_s, add2(raw.pair(k), minus_lo)).get();
+        float2 n = nf[k].get();
+        auto odd = [](float x) { return __float_as_uint(x + kMagic) & 1u; };
+        if (fabsf(e.x) > hs || (fabsf(e.x) == hs && odd(n.x))) n.x += copysignf(1.f, e.x);
+        if (fabsf(e.y) > hs || (fabsf(e.y) == hs && odd(n.y))) n.y += copysignf(1.f, e.y);
+        nf[k] = F2(n.x, n.y);
       }
     }
   } else {
@@ -212,43 +222,45 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
     // 2^-24 relative), rounded by adding kMagic.  A value nearer than twice that to a half step takes
     // the exact path below.
     const float tie = 0.5f - (2.f * kQ + fabsf(g.off)) * 1.1920929e-7f;
+    const F2 off(g.off), minus(-1.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = fmaf(x[i], g.inv, g.off), r = f + kMagic;
-      bits[i] = __float_as_uint(r);
-      nf[i] = r - kMagic;
-      near = fmaxf(near, fabsf(f - nf[i]));
+    for (int k = 0; k < 4; ++k) {
+      const F2 f = fma2(raw.pair(k), inv, off);
+      nf[k] = add2(add2(f, magic), unmagic);
+      const float2 e = fma2(nf[k], minus, f).get();
+      near = fmaxf(near, fmaxf(fabsf(e.x), fabsf(e.y)));
     }
     exact |= !(near < tie);
   }
   if (exact && g.usable) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    auto code = [&](float x) {
       // t + te = x - lo exactly; n the nearest code up to one; m = t - n s exactly (n s has 19 bits and
       // is within s of t); so the sign of 2 (m + te) -+ s is known
-      const float t = x[i] - g.lo, z = t - x[i], te = (x[i] - (t - z)) + (-g.lo - z);
+      const float t = x - g.lo, z = t - x, te = (x - (t - z)) + (-g.lo - z);
       float n = fminf(fmaxf(t * g.inv, -1.f), kQ + 1.f);
       n = (n + kMagic) - kMagic;
       const float m = fmaf(-n, g.s, t), above = (2.f * m - g.s) + 2.f * te, below = (2.f * m + g.s) + 2.f * te;
       const bool odd = __float_as_uint(n + kMagic) & 1u;
       if (above > 0.f || (above == 0.f && odd)) n += 1.f;
       else if (below < 0.f || (below == 0.f && odd)) n -= 1.f;
-      n = fminf(fmaxf(n, 0.f), kQ);
-      nf[i] = n;
-      bits[i] = __float_as_uint(n + kMagic);
+      return fminf(fmaxf(n, 0.f), kQ);
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = raw.pair(k).get();
+      nf[k] = F2(code(x.x), code(x.y));
     }
   }
-  // sum of code_i << (BITS * i), the magic bits taken off once (arithmetic modulo 2^32)
-  constexpr int kPer = 32 / BITS;
-#pragma unroll
-  for (int j = 0; j < BITS / 4; ++j) {
-    uint32_t w = 0, m = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      w += bits[j * kPer + i] << (BITS * i);
-      m += kMagicBits << (BITS * i);
-    }
-    c.w[j] = w - m;
+  // four codes (two of 8 bits) in one fp32 number, whose integer then lies in its low mantissa bits
+  const F2 bias(8388608.f);
+  auto words = [&](F2 x) { const float2 y = add2(x, bias).get(); return make_uint2(__float_as_uint(y.x), __float_as_uint(y.y)); };
+  if constexpr (BITS == 4) {
+    const uint2 y = words(fma2(nf[3], F2(4096.f), fma2(nf[2], F2(256.f), fma2(nf[1], F2(16.f), nf[0]))));
+    c.w[0] = __byte_perm(y.x, y.y, 0x5410);
+  } else {
+    const uint2 a = words(fma2(nf[1], F2(256.f), nf[0])), b = words(fma2(nf[3], F2(256.f), nf[2]));
+    c.w[0] = __byte_perm(a.x, b.x, 0x5410);
+    c.w[1] = __byte_perm(a.y, b.y, 0x5410);
   }
 }
 
@@ -299,29 +311,32 @@ __global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k,
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool is_v = warp >= 2;
-  const int rsub = (warp & 1) * RPW + lane / LPR, l16 = lane % LPR, grp = l16 / 4, cell = l16 % 4 * 2 * G + grp;
+  const int rsub = (warp & 1) * RPW + lane / LPR, l16 = lane % LPR, grp = l16 / 4, cell = l16 % 4 * G + grp;
+  const int ch = grp * 64 + l16 % 4 * 8;   // the lane's channels: 8 from here on, and 8 that lie 32 further (every access whole sectors)
   const Rows& src = is_v ? v : k;
   const char* in = static_cast<const char*>(src.p) +
-                   sizeof(T) * (p.layer * src.layer + p.b * src.seq + p.h * src.head + l16 * 16);
+                   sizeof(T) * (p.layer * src.layer + p.b * src.seq + p.h * src.head + ch);
   const size_t row0 = row0_of(a, a.layer0 + p.layer, pid, p.h);
   uint8_t* code = (is_v ? a.v_code : a.k_code) + row0 * ROW + cell * BITS;
   __half2* scale = (is_v ? a.v_scale : a.k_scale) + row0 * G + grp;
   const bool mean = p.s1 == a.page && a.k_mean != nullptr;
   // Rows of slot t belong to the lanes with rsub = t mod STEP, and a lane sums s n and lo of its rows
   // in their order, so a page's mean is one sum however its tokens arrived.
-  float acc[16], los = 0.f;
+  F2 acc[2][4];
+  float los = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = F2(0.f);
   if (mean && !is_v)
     for (int t = rsub; t < p.s0; t += STEP) {
       Cell<BITS> c[2];
       c[0].load(code + (size_t)t * ROW);
-      c[1].load(code + (size_t)t * ROW + G * BITS);
+      c[1].load(code + (size_t)t * ROW + 4 * G * BITS);
       const __half2 meta = scale[(size_t)t * G];
-      const float s = __low2float(meta);
+      const F2 s(__low2float(meta));
       los += __high2float(meta);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = fmaf(s, (float)c[i / 8].code(i % 8), acc[i]);
+      for (int i = 0; i < 8; ++i)
+        acc[i / 4][i % 4] = fma2(s, F2((float)c[i / 4].code(i % 4), (float)c[i / 4].code(i % 4 + 4)), acc[i / 4][i % 4]);
     }
   for (int base = p.s0 & ~(STEP - 1); base < p.s1; base += STEP * FLY) {
     Raw8<T> raw[FLY][2];
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k,
       if (t >= p.s0 && t < p.s1) {
         const char* at = in + sizeof(T) * ((int64_t)(p.tok0 + t) * src.tok);
         raw[u][0].load(at);
-        raw[u][1].load(at + 8 * sizeof(T));
+        raw[u][1].load(at + 32 * sizeof(T));
       } else {
         raw[u][0].zero();
         raw[u][1].zero();
@@ -348,13 +363,13 @@ __global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k,
       los += sc.lo;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float nf[8];
+        F2 nf[4];
         Cell<BITS> c;
         codes_of<T, BITS>(raw[u][j], sc, c, nf);
-        c.store(code + (size_t)t * ROW + j * G * BITS);
+        c.store(code + (size_t)t * ROW + j * 4 * G * BITS);
         if (mean && !is_v) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[8 * j + i] = fmaf(sc.s, nf[i], acc[8 * j + i]);
+          for (int k = 0; k < 4; ++k) acc[j][k] = fma2(F2(sc.s), nf[k], acc[j][k]);
         }
       }
     }
@@ -362,7 +377,11 @@ __global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k,
   if (!mean) return;   // the same for the whole CTA
   if (!is_v) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sums[rsub][l16 * 16 + i] = acc[i] + los;
+    for (int i = 0; i < 8; ++i) {
+      const float2 y = acc[i / 4][i % 4].get();
+      sums[rsub][ch + i / 4 * 32 + i % 4] = y.x + los;
+      sums[rsub][ch + i / 4 * 32 + i % 4 + 4] = y.y + los;
+    }
   }
   __syncthreads();
   __nv_bfloat16* out = a.k_mean + (row0 >> a.page_log2) * D;

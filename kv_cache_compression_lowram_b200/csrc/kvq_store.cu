@@ -18,10 +18,6 @@ namespace lowram {
 namespace kvq {
 namespace {
 
-#ifndef KVQ_FLY
-#define KVQ_FLY 2
-#define KVQ_WB 6
-#endif
 constexpr int kThreads = 128;
 constexpr int kUnroll = 4;   // rows that a lane of the reading kernel has in flight
 constexpr unsigned kAll = 0xffffffffu;
@@ -33,6 +29,12 @@ constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// max(|a|, |b|, |c|), not NaN unless all are
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -204,7 +206,7 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
       const F2 t = add2(raw.pair(k), minus_lo);
       nf[k] = add2(fma2(t, inv, magic), unmagic);
       const float2 e = fma2(nf[k], minus_s, t).get();
-      near = fmaxf(near, fmaxf(fabsf(e.x), fabsf(e.y)));
+      near = max_abs(near, e.x, e.y);
     }
     if (near >= hs) {
 #pragma unroll
@@ -228,7 +230,7 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
       const F2 f = fma2(raw.pair(k), inv, off);
       nf[k] = add2(add2(f, magic), unmagic);
       const float2 e = fma2(nf[k], minus, f).get();
-      near = fmaxf(near, fmaxf(fabsf(e.x), fabsf(e.y)));
+      near = max_abs(near, e.x, e.y);
     }
     exact |= !(near < tie);
   }
@@ -298,17 +300,13 @@ __device__ __forceinline__ bool piece_of(const Args& a, const int32_t* pos, cons
 }
 
 template <typename T, int BITS, int D>
-__global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 6) write_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
                                                          const int32_t* __restrict__ count, int pieces) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 2 * RPW, G = D / kGroup, ROW = D * BITS / 8, FLY = KVQ_FLY;
+  constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 2 * RPW, G = D / kGroup, ROW = D * BITS / 8, FLY = 2;
   __shared__ float sums[STEP][D];
   Piece p;
   if (!piece_of(a, pos, count, pieces, &p)) return;
   const int pid = p.page < 0 ? -1 : page_of(a, p.b, p.page);
-  if (pid < 0) {
-    if (p.page >= 0 && threadIdx.x == 0) flag(a, KVQ_ERR_PAGE);
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool is_v = warp >= 2;
   const int rsub = (warp & 1) * RPW + lane / LPR, l16 = lane % LPR, grp = l16 / 4, cell = l16 % 4 * G + grp;
@@ -316,6 +314,28 @@ __global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k,
   const Rows& src = is_v ? v : k;
   const char* in = static_cast<const char*>(src.p) +
                    sizeof(T) * (p.layer * src.layer + p.b * src.seq + p.h * src.head + ch);
+  // FLY rows of a lane are on their way from here on (the table's answer is not needed for them)
+  int ahead = (p.s0 & ~(STEP - 1)) + rsub;
+  in += sizeof(T) * ((int64_t)(p.tok0 + ahead) * src.tok);
+  const int64_t in_step = (int64_t)sizeof(T) * STEP * src.tok;
+  Raw8<T> raw[FLY][2];
+  auto fetch = [&](Raw8<T> (&r)[2]) {
+    if (ahead >= p.s0 && ahead < p.s1) {
+      r[0].load(in);
+      r[1].load(in + 32 * sizeof(T));
+    } else {
+      r[0].zero();
+      r[1].zero();
+    }
+    ahead += STEP;
+    in += in_step;
+  };
+#pragma unroll
+  for (int u = 0; u < FLY; ++u) fetch(raw[u]);
+  if (pid < 0) {
+    if (p.page >= 0 && threadIdx.x == 0) flag(a, KVQ_ERR_PAGE);
+    return;
+  }
   const size_t row0 = row0_of(a, a.layer0 + p.layer, pid, p.h);
   uint8_t* code = (is_v ? a.v_code : a.k_code) + row0 * ROW + cell * BITS;
   __half2* scale = (is_v ? a.v_scale : a.k_scale) + row0 * G + grp;
@@ -338,40 +358,35 @@ __global__ void __launch_bounds__(kThreads, KVQ_WB) write_kernel(Args a, Rows k,
       for (int i = 0; i < 8; ++i)
         acc[i / 4][i % 4] = fma2(s, F2((float)c[i / 4].code(i % 4), (float)c[i / 4].code(i % 4 + 4)), acc[i / 4][i % 4]);
     }
-  for (int base = p.s0 & ~(STEP - 1); base < p.s1; base += STEP * FLY) {
-    Raw8<T> raw[FLY][2];
+  int t = (p.s0 & ~(STEP - 1)) + rsub;
+  code += (size_t)t * ROW;
+  scale += (size_t)t * G;
+  for (int base = p.s0 & ~(STEP - 1); base < p.s1;) {
 #pragma unroll
     for (int u = 0; u < FLY; ++u) {
-      const int t = base + u * STEP + rsub;
-      if (t >= p.s0 && t < p.s1) {
-        const char* at = in + sizeof(T) * ((int64_t)(p.tok0 + t) * src.tok);
-        raw[u][0].load(at);
-        raw[u][1].load(at + 32 * sizeof(T));
-      } else {
-        raw[u][0].zero();
-        raw[u][1].zero();
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < FLY; ++u) {
-      const int t = base + u * STEP + rsub;
-      if (base + u * STEP >= p.s1) break;
+      if (base >= p.s1) break;             // the same for the whole CTA
       __half2 meta;
       const Scale sc = scale_of<T, BITS>(group_range(raw[u]), meta);
-      if (t < p.s0 || t >= p.s1) continue;
-      if ((l16 & 3) == 0) scale[(size_t)t * G] = meta;
-      los += sc.lo;
+      if (t >= p.s0 && t < p.s1) {
+        if ((l16 & 3) == 0) *scale = meta;
+        los += sc.lo;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        F2 nf[4];
-        Cell<BITS> c;
-        codes_of<T, BITS>(raw[u][j], sc, c, nf);
-        c.store(code + (size_t)t * ROW + j * 4 * G * BITS);
-        if (mean && !is_v) {
+        for (int j = 0; j < 2; ++j) {
+          F2 nf[4];
+          Cell<BITS> c;
+          codes_of<T, BITS>(raw[u][j], sc, c, nf);
+          c.store(code + j * 4 * G * BITS);
+          if (mean && !is_v) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[j][k] = fma2(F2(sc.s), nf[k], acc[j][k]);
+            for (int k = 0; k < 4; ++k) acc[j][k] = fma2(F2(sc.s), nf[k], acc[j][k]);
+          }
         }
       }
+      fetch(raw[u]);
+      base += STEP;
+      t += STEP;
+      code += STEP * ROW;
+      scale += STEP * G;
     }
   }
   if (!mean) return;   // the same for the whole CTA

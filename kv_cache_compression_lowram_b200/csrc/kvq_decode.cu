@@ -127,20 +127,29 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
     const int nc = min(kChunk, n - i0);
     if (i0) __syncthreads();
     for (int j = warp; j < rows; j += kWarps) {
+      // up to 64 parts at once, in registers
+      float m = -INFINITY, l = 0.f, mp[2], lp[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool in = lane + 32 * k < nc;
+        const float* p = at(i0 + (in ? lane + 32 * k : 0)) + ROWS * D + j;
+        mp[k] = in ? __ldcg(p) : -INFINITY;
+        lp[k] = __ldcg(p + ROWS);
+      }
       if (i0 == 0) {
-        float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(at(i) + ROWS * D + j));
+        m = fmaxf(mp[0], mp[1]);
+        for (int i = lane + 64; i < n; i += 32) m = fmaxf(m, __ldcg(at(i) + ROWS * D + j));
         m = warp_max(m);
         if (lane == 0) norm[j] = m;
+      } else {
+        m = norm[j];
       }
-      __syncwarp();
-      const float mj = norm[j];
-      float l = 0.f;
-      for (int i = lane; i < nc; i += 32) {
+      for (int i = lane, k = 0; i < nc; i += 32, ++k) {
         const float* p = at(i0 + i) + ROWS * D + j;
-        const float mp = __ldcg(p), lp = __ldcg(p + ROWS), w = mp == -INFINITY ? 0.f : ex2(mp - mj);
+        const float mi = k == 0 ? mp[0] : (k == 1 ? mp[1] : __ldcg(p)), li = k == 0 ? lp[0] : (k == 1 ? lp[1] : __ldcg(p + ROWS));
+        const float w = mi == -INFINITY ? 0.f : ex2(mi - m);
         wt[i * ROWS + j] = w;
-        l += w == 0.f ? 0.f : w * lp;
+        l += w == 0.f ? 0.f : w * li;
       }
       l = warp_sum(l);
       if (lane == 0) norm[ROWS + j] = i0 ? norm[ROWS + j] + l : l;

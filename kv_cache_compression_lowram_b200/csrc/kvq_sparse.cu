@@ -1,6 +1,6 @@
 // Quantised KV cache: attention over the pages that their mean keys select for each query.
 //
-// One launch.  A unit -- (layer, sequence, query token, KV head) -- belongs to a cluster of 1 to 16
+// One launch.  A unit -- (layer, sequence, query token, KV head) -- belongs to a cluster of 1 to 8
 // CTAs, which do all of it together through each other's shared memory:
 //   1. each CTA scores its share of the full pages (mean key . sum of the group's queries, in 64
 //      bits) into its shared memory: 2 d bytes a page, the larger part of what a long context costs;
@@ -22,7 +22,7 @@ namespace lowram {
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 1024;
 constexpr int kRank = 256;    // members of a border bin that are ranked by comparison
@@ -31,13 +31,13 @@ template <int BITS, int D, int ROWS, bool F32> struct Plan {
   using Tl = Tile<BITS, D, ROWS, F32>;
   static constexpr int TB = Tl::BLOCK <= 2304 ? 2 : 1;
   static constexpr int SLOT = TB * Tl::BLOCK;
-  static constexpr int STAGES = SLOT > 4608 ? 2 : 3;
+  static constexpr int STAGES = 2;
   static constexpr int RING = kWarps * STAGES * SLOT;
   static constexpr int JOIN = kWarps * ROWS * D * 4;
   // what lives at once: the ring and the joined sums, or the scores and the histogram
   static constexpr int ATTEND = RING + JOIN + Tl::QFRAG;
   static constexpr int SMALL = Tl::QMETA + kWarps * ROWS * 8 + 2 * ROWS * 4;
-  static constexpr int MINB = ATTEND <= 72 * 1024 ? 3 : (ATTEND <= 108 * 1024 ? 2 : 1);
+  static constexpr int MINB = ATTEND <= 100 * 1024 ? 2 : 1;
 };
 
 // Scores: NaN counts as -infinity, -0 as 0.
@@ -269,7 +269,7 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
   if (top_k <= last) {
     // 1. scores of the full pages [c0, c1)
     const int share = (last + CS - 1) / CS, c0 = min(rank * share, last), c1 = min(c0 + share, last);
-    constexpr int LPP = D / 8, PPW = 32 / LPP, FLY = 32 / PPW < 16 ? 32 / PPW : 16, STEP = PPW * FLY;   // 32 or 16 pages
+    constexpr int LPP = D / 8, PPW = 32 / LPP, FLY = 8, STEP = PPW * FLY;   // 32, 16 or 8 pages
     const int c8 = lane % LPP;
     if (top_k > 1) {
       auto ask = [&](int base) {
@@ -281,29 +281,46 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
       double qs[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) qs[k] = 0.0;
-      for (int j = 0; j < a.g; ++j) {
-        const T* src = q + (size_t)j * D + c8 * 8;
-        __align__(16) T x[8];
+#pragma unroll 1
+      for (int j = 0; j < a.g; j += 4) {   // four rows on their way at once
+        __align__(16) T x[4][8];
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(x) / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
+        for (int r = 0; r < 4; ++r) {
+          const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)min(j + r, a.g - 1) * D + c8 * 8);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) qs[k] += (double)to_f<T>(x[k]);
+          for (int k = 0; k < (int)sizeof(x[0]) / 16; ++k) reinterpret_cast<uint4*>(x[r])[k] = __ldg(src + k);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (j + r < a.g) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) qs[k] += (double)to_f<T>(x[r][k]);
+          }
       }
       const uint32_t row = (uint32_t)(row0_of(a, a.layer0 + layer, 0, h) >> a.page_log2);
-      for (int base = c0 + warp * STEP; base < c1; base += kWarps * STEP) {
+      // two steps' pages are on their way while a third's places are looked up
+      uint4 w[FLY];
+      auto fetch = [&]() {
         if (pid == -1) flag(a, KVQ_ERR_PAGE);
-        uint4 w[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
           const int p = __shfl_sync(kFull, pid, f * PPW + lane / LPP);
           w[f] = make_uint4(0x7fc07fc0u, 0, 0, 0);   // a page that is not there scores NaN
           if (p >= 0) w[f] = __ldg(reinterpret_cast<const uint4*>(a.k_mean + (size_t)(row + (uint32_t)p * a.Hkv) * D) + c8);
         }
-        pid = ask(base + kWarps * STEP);
+      };
+      fetch();
+      pid = ask(c0 + (warp + kWarps) * STEP);
+      for (int base = c0 + warp * STEP; base < c1; base += kWarps * STEP) {
+        uint4 now[FLY];
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) now[f] = w[f];
+        fetch();
+        pid = ask(base + 2 * kWarps * STEP);
         double x[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
-          const uint32_t v[4] = {w[f].x, w[f].y, w[f].z, w[f].w};
+          const uint32_t v[4] = {now[f].x, now[f].y, now[f].z, now[f].w};
           x[f] = 0.0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -311,12 +328,11 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
             x[f] = fma(qs[2 * k + 1], (double)__uint_as_float(v[k] & 0xffff0000u), x[f]);
           }
         }
-        // sums over the LPP lanes of a page: lanes trade halves of their pages, and with `bits` trades
-        // done a lane holds the pages whose low bits are its own
-        constexpr int TRADES = FLY == 16 ? 4 : 3;
+        // sums over the LPP lanes of a page: lanes trade halves of their pages, and after three trades a
+        // lane holds one page, whose bits its own low bits chose
         int have = FLY;
 #pragma unroll
-        for (int t = 0; t < TRADES; ++t) {
+        for (int t = 0; t < 3; ++t) {
           have >>= 1;
           const int o = 1 << t;
           const bool up = lane & o;
@@ -328,18 +344,14 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
             }
         }
 #pragma unroll
-        for (int o = 1 << TRADES; o < LPP; o <<= 1) x[0] += __shfl_xor_sync(kFull, x[0], o);
-        // page f of this lane: bit t of the lane chose the half of size FLY >> (t + 1)
-        int f = 0;
-#pragma unroll
-        for (int t = 0; t < TRADES; ++t) f += (lane >> t & 1) * (FLY >> (t + 1));
-        const int c = base + f * PPW + lane / LPP;
-        if (c8 < (1 << TRADES) && c < c1) mine[c - c0] = plain_score(x[0]);
+        for (int o = 8; o < LPP; o <<= 1) x[0] += __shfl_xor_sync(kFull, x[0], o);
+        const int f = (lane & 1) * 4 + (lane & 2) + (lane >> 2 & 1), c = base + f * PPW + lane / LPP;
+        if (c8 < 8 && c < c1) mine[c - c0] = plain_score(x[0]);
       }
       // 2. everyone's scores, and the best of them
       cluster.sync();
       int mn = INT_MAX, mx = INT_MIN;
-#pragma unroll 4
+#pragma unroll 8
       for (int c = tid; c < last; c += kThreads) {
         const int r = c / share, k = key_of((float)cluster.map_shared_rank(mine, r)[c - r * share]);
         keys[c] = k;
@@ -518,7 +530,7 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
 template <int BITS, int D, int ROWS, bool F32>
 cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, void* out, int32_t* sel, cudaStream_t s) {
   using P = Plan<BITS, D, ROWS, F32>;
-  static int fits[64][5] = {{0}};   // per device: clusters of 1, 2, 4, 8, 16 CTAs resident at once, plus one
+  static int fits[64][4] = {{0}};   // per device: clusters of 1, 2, 4, 8 CTAs resident at once, plus one
   auto kernel = sparse_kernel<BITS, D, ROWS, F32>;
   const unsigned units = (unsigned)a.n_layers * a.B * a.n * a.Hkv;
   int dev = 0;
@@ -536,17 +548,16 @@ cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, voi
     const int scores = share_room(cs) * 8 + (a.max_pages * 4 + 7) / 8 * 8;
     return (scores > P::ATTEND ? scores : P::ATTEND) + (a.max_pages + 31) / 32 * 4 + top_k * 4 + P::SMALL + 16;
   };
-  int now[5];
+  int now[4];
   int* fit = dev < 64 ? fits[dev] : now;
   if (dev >= 64 || !fit[0]) {
-    int room = 0, found[5];
+    int room = 0, found[4];
     if ((e = cudaDeviceGetAttribute(&room, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room - (int)fa.sharedSizeBytes)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
     cfg.dynamicSmemBytes = P::ATTEND + 4096 + P::SMALL;
-    for (int k = 0; k < 5; ++k) {
+    for (int k = 0; k < 4; ++k) {
       cfg.gridDim = 1 << k;
       attr.val.clusterDim.x = 1 << k;
       attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
@@ -554,10 +565,10 @@ cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, voi
       if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
       found[k] = n + 1;
     }
-    for (int k = 4; k >= 0; --k) fit[k] = found[k];
+    for (int k = 3; k >= 0; --k) fit[k] = found[k];
   }
   // the largest cluster that leaves all units resident at once
-  int k = 4;
+  int k = 3;
   while (k > 0 && (int)units > (fit[k] - 1)) --k;
 #ifdef KVQ_CS
   k = KVQ_CS;

@@ -41,9 +41,6 @@
 namespace lowram {
 namespace kvq {
 
-#ifndef KVQ_QMAX
-#define KVQ_QMAX 16
-#endif
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -140,7 +137,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   static constexpr int BLOCK = 2 * (CODE + META);
   static constexpr int QFRAG = STEPS * NT * SPQ * 32 * 8;       // bytes of the queries' B operands
   static constexpr int QMETA = ROWS * (1 + G) * 4;              // f'' and the group sums
-  static constexpr bool QREG = STEPS * NT * SPQ * 2 <= KVQ_QMAX;       // B operands kept in registers
+  static constexpr bool QREG = STEPS * NT * SPQ * 2 <= 16;       // B operands kept in registers
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   // A score may pass the running maximum by a factor of 2^kSlack in its weight, a value scale leave
   // [2^E, 2^(E+1)) by a factor of kWide either way: w <= 2^(kSlack + 1) kWide kBias < 2^16, and what

@@ -2,11 +2,14 @@
 //
 // One launch.  A unit -- (layer, sequence, query token, KV head) -- belongs to a cluster of 1 to 8
 // CTAs, which do all of it together through each other's shared memory:
-//   1. each CTA scores its share of the full pages (mean key . sum of the group's queries, in 64
-//      bits) into its shared memory: 2 d bytes a page, the larger part of what a long context costs;
-//   2. every CTA gathers all scores, rounded to fp32, and finds the same top_k - 1 best pages: one
-//      histogram over the range of the scores leaves a bin that holds the border, whose few members
-//      are ranked by their 64-bit scores (a bin too large for that is cut again);
+//   1. each CTA scores its share of the full pages (mean key . sum of the group's queries) into its
+//      shared memory: 2 d bytes a page, the larger part of what a long context costs.  In fp32, with a
+//      bound on how far that is from the score in 64 bits that selection goes by: conversions to fp64
+//      would take three times as long as the loads;
+//   2. every CTA gathers all scores and finds the same top_k - 1 best pages: a histogram over the
+//      range of the scores leaves a bin that holds the border (a bin of many pages is cut again);
+//      pages further from it than twice the bound are decided, and the few others are scored once
+//      more in fp64 and ranked by comparison;
 //   3. the selected pages' 16-token blocks go round the warps of the cluster, as in the attention
 //      over whole sequences; CTAs join their sums and the cluster joins the CTAs'.
 // No workspace, no second launch, and nothing is written but the outputs.
@@ -40,17 +43,17 @@ template <int BITS, int D, int ROWS, bool F32> struct Plan {
   static constexpr int MINB = ATTEND <= 100 * 1024 ? 2 : 1;
 };
 
-// Scores: NaN counts as -infinity, -0 as 0.
-__device__ __forceinline__ double plain_score(double s) { return s == s ? s + 0.0 : -INFINITY; }
 // Integers in the order of the numbers, and back.
 __device__ __forceinline__ int key_of(float f) {
   const int b = __float_as_int(f);
   return b ^ (b < 0 ? 0x7fffffff : 0);
 }
 __device__ __forceinline__ float float_of(int k) { return __int_as_float(k ^ (k < 0 ? 0x7fffffff : 0)); }
-__device__ __forceinline__ long long key_of(double s) {
-  const long long b = __double_as_longlong(s);
-  return b ^ (b < 0 ? 0x7fffffffffffffffll : 0);
+// The same of a score, 0 the smallest; NaN counts as -infinity, -0 as 0.
+__device__ __forceinline__ double plain_score(double s) { return s == s ? s + 0.0 : -INFINITY; }
+__device__ __forceinline__ unsigned long long bits_of(double s) {
+  const unsigned long long b = (unsigned long long)__double_as_longlong(s);
+  return b ^ (b >> 63 ? ~0ull : 1ull << 63);
 }
 
 struct Select {   // shared by the CTA while it selects
@@ -58,10 +61,11 @@ struct Select {   // shared by the CTA while it selects
   int wide[2][kWarps];
   unsigned sums[kWarps];
   int border, above, members, list[kRank];
+  float bound[kWarps];   // of the norms of this CTA's means (read by the cluster)
   double score[kRank];
 };
 
-// How many of the keys of threads 0 .. this one are counted in `x`, this one included.
+// x summed over the threads up to this one.  A barrier is inside; `sums` may be written anew after the next.
 __device__ __forceinline__ unsigned scan_cta(unsigned x, unsigned* sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -74,56 +78,70 @@ __device__ __forceinline__ unsigned scan_cta(unsigned x, unsigned* sums) {
   for (int w = 0; w < warp; ++w) x += sums[w];
   return x;
 }
+__device__ __forceinline__ unsigned sum_cta(unsigned x, unsigned* sums) {
+  x = __reduce_add_sync(kFull, x);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) x += sums[w];
+  __syncthreads();
+  return x;
+}
+__device__ __forceinline__ void range_cta(int& mn, int& mx, int (&wide)[2][kWarps]) {
+  mx = __reduce_max_sync(kFull, mx);
+  mn = __reduce_min_sync(kFull, mn);
+  if ((threadIdx.x & 31) == 0) {
+    wide[0][threadIdx.x >> 5] = mx;
+    wide[1][threadIdx.x >> 5] = mn;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    mx = max(mx, wide[0][w]);
+    mn = min(mn, wide[1][w]);
+  }
+}
 
 // Marks (bits of `mark`, zeroed here) the `want` largest of n scores, 0 < want < n; equal ones from the
-// lowest index on.  keys[i]: score i rounded to fp32, as key_of(); exact(i): score i; mn, mx: this
-// thread's smallest and largest key of all.  All threads of the CTA.
+// lowest index on.  keys[i]: score i to within `off`, as key_of(); mn, mx: this thread's smallest and
+// largest key; exact(members): makes s.score[j] score s.list[j] for all j.  False (and nothing marked)
+// where more than kRank pages are too near to one another for that.  All threads of the CTA.
 template <class Exact>
-__device__ __forceinline__ void select_largest(const int* keys, int n, int want, int mn, int mx, unsigned* mark, Select& s, Exact exact) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__device__ __forceinline__ bool select_largest(const int* keys, int n, int want, float off, int mn, int mx, unsigned* mark, Select& s, Exact exact) {
+  const int tid = threadIdx.x;
   for (int i = tid; i < (n + 31) / 32; i += kThreads) mark[i] = 0;
-  int lo = INT_MIN, hi = INT_MAX;        // the keys still in question
+  int lo = INT_MIN, hi = INT_MAX, left = want;   // the keys that may be the want-th, and its place among them
   bool linear = true;
   for (;;) {
-    mx = __reduce_max_sync(kFull, mx);
-    mn = __reduce_min_sync(kFull, mn);
-    if (lane == 0) {
-      s.wide[0][warp] = mx;
-      s.wide[1][warp] = mn;
-    }
     for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
     if (tid == 0) s.members = 0;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      mx = max(mx, s.wide[0][w]);
-      mn = min(mn, s.wide[1][w]);
-    }
+    range_cta(mn, mx, s.wide);
     // bins: even in the scores at first (unless one is infinite), then even in the keys
     const float smin = float_of(mn), span = float_of(mx) - smin, scale = (kBins - 1) / span;
     linear = linear && span > 0.f && span < 1e38f && scale < 1e38f;
     const unsigned width = (unsigned)mx - (unsigned)mn;
     const int shift = max(0, 22 - __clz((int)width));
     auto bin_of = [&](int k) { return linear ? min((int)((float_of(k) - smin) * scale), kBins - 1) : (int)(((unsigned)k - (unsigned)mn) >> shift); };
-#pragma unroll 4
+#pragma unroll 2
     for (int i = tid; i < n; i += kThreads) {
       const int k = keys[i];
       if (k >= lo && k <= hi) atomicAdd(&s.hist[bin_of(k)], 1u);
     }
     __syncthreads();
-    // the bin of the want-th largest: thread t sums bins from the top, kBins / kThreads each
+    // the bin of the left-th largest: thread t sums bins from the top, kBins / kThreads each
     constexpr int PER = kBins / kThreads;
     unsigned sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) sum += s.hist[kBins - 1 - tid * PER - i];
     const unsigned inc = scan_cta(sum, s.sums);
     unsigned before = inc - sum;
-    if (before < (unsigned)want && inc >= (unsigned)want) {   // one thread
+    if (before < (unsigned)left && inc >= (unsigned)left) {   // one thread
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int b = kBins - 1 - tid * PER - i;
         const unsigned h = s.hist[b];
-        if (before < (unsigned)want && before + h >= (unsigned)want) {
+        if (before < (unsigned)left && before + h >= (unsigned)left) {
           s.border = b;
           s.above = before;
         }
@@ -131,97 +149,85 @@ __device__ __forceinline__ void select_largest(const int* keys, int n, int want,
       }
     }
     __syncthreads();
-    const int border = s.border, inside = s.hist[border];
-    want -= s.above;
-    const bool rank = inside <= kRank, equal = mx == mn;
-    int nlo = INT_MAX, nhi = INT_MIN;
-#pragma unroll 4
+    const int border = s.border;
+    left -= s.above;
+    const bool few = s.hist[border] <= kRank || mn == mx;
+    int nlo = INT_MAX, nhi = INT_MIN;      // the border bin's keys
+#pragma unroll 2
     for (int i = tid; i < n; i += kThreads) {
       const int k = keys[i];
-      if (!(k >= lo && k <= hi)) continue;
-      const int b = bin_of(k);
-      if (b > border) atomicOr(&mark[i >> 5], 1u << (i & 31));
-      else if (b == border) {
-        if (rank) {
-          const int at = atomicAdd(&s.members, 1);
-          s.list[at] = i;
-          s.score[at] = exact(i);
-        }
+      if (k >= lo && k <= hi && bin_of(k) == border) {
         nlo = min(nlo, k);
         nhi = max(nhi, k);
       }
     }
     __syncthreads();
-    if (rank) {
-      for (int j = tid; j < inside; j += kThreads) {
-        const int i = s.list[j];
-        const double x = s.score[j];
-        int r = 0;
-        for (int t = 0; t < inside; ++t) r += s.score[t] > x || (s.score[t] == x && s.list[t] < i);
-        if (r < want) atomicOr(&mark[i >> 5], 1u << (i & 31));
-      }
-      __syncthreads();
-      return;
-    }
-    if (equal) break;
-    mn = lo = nlo;                         // the border bin alone, by its keys (the CTA's range: next round)
-    mx = hi = nhi;
-    lo = __reduce_min_sync(kFull, lo);
-    hi = __reduce_max_sync(kFull, hi);
-    if (lane == 0) {
-      s.wide[0][warp] = hi;
-      s.wide[1][warp] = lo;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      hi = max(hi, s.wide[0][w]);
-      lo = min(lo, s.wide[1][w]);
-    }
+    mn = nlo;
+    mx = nhi;
+    range_cta(nlo, nhi, s.wide);
+    lo = nlo;
+    hi = nhi;
     linear = false;
     __syncthreads();
+    if (few) break;
   }
-  // More than kRank scores are one fp32 number: the want-th largest of them, bit by bit from the top of
-  // their 64-bit keys, then the equal ones from the lowest index on.
-  const int same = mx;
-  auto bits = [&](int i) { return (unsigned long long)key_of(exact(i)) ^ 1ull << 63; };   // 0 the smallest
-  if (tid == 0) s.members = -1;
+  // the want-th largest of the keys lies in [lo, hi]: that of the scores is within `off` of it
+  const float over = float_of(hi) + 2.f * off, under = float_of(lo) - 2.f * off;
+  unsigned in = 0;
+#pragma unroll 2
+  for (int i = tid; i < n; i += kThreads) {
+    const float x = float_of(keys[i]);
+    if (x > over) {
+      atomicOr(&mark[i >> 5], 1u << (i & 31));
+      ++in;
+    } else if (!(x < under)) {
+      const int at = atomicAdd(&s.members, 1);
+      if (at < kRank) s.list[at] = i;
+    }
+  }
+  want -= sum_cta(in, s.sums);
+  const int members = s.members;
+  if (members > kRank) return false;
+  exact(members);
   __syncthreads();
-  for (int i = tid; i < n; i += kThreads)
-    if (keys[i] == same) atomicMax(&s.members, i);
+  for (int j = tid; j < members; j += kThreads) {
+    const int i = s.list[j];
+    const double x = s.score[j];
+    int r = 0;
+    for (int t = 0; t < members; ++t) r += s.score[t] > x || (s.score[t] == x && s.list[t] < i);
+    if (r < want) atomicOr(&mark[i >> 5], 1u << (i & 31));
+  }
   __syncthreads();
-  const unsigned long long one = bits(s.members);
-  bool differ = false;                     // mostly they are one 64-bit number too
-  for (int i = tid; i < n; i += kThreads) differ |= keys[i] == same && bits(i) != one;
+  return true;
+}
+
+// The same without bounds, for scores too near to one another (mostly equal ones): the want-th largest
+// bit by bit from the top of its 64-bit key, then equal ones from the lowest index on.
+template <class Score> __device__ __noinline__ void select_exactly(int n, int want, unsigned* mark, Select& s, Score score) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < (n + 31) / 32; i += kThreads) mark[i] = 0;
+  auto bits = [&](int i) { return bits_of(score(i)); };
+  const unsigned long long one = bits(0);
+  bool differ = false;
+  for (int i = tid; i < n; i += kThreads) differ |= bits(i) != one;
   differ = __syncthreads_or(differ);
   unsigned long long top = differ ? 0 : one;   // the bits so far
   for (int bit = differ ? 63 : -1; bit >= 0; --bit) {
     const unsigned long long next = top | 1ull << bit;
     unsigned c = 0;
-    for (int i = tid; i < n; i += kThreads) c += keys[i] == same && bits(i) >= next;
-    c = __reduce_add_sync(kFull, c);
-    if (lane == 0) s.sums[warp] = c;
-    __syncthreads();
-    c = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) c += s.sums[w];
-    if (c >= (unsigned)want) top = next;
-    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) c += bits(i) >= next;
+    if (sum_cta(c, s.sums) >= (unsigned)want) top = next;
   }
   unsigned over = 0;
   for (int i = tid; i < n; i += kThreads)
-    if (keys[i] == same && bits(i) > top) {
+    if (bits(i) > top) {
       atomicOr(&mark[i >> 5], 1u << (i & 31));
       ++over;
     }
-  over = __reduce_add_sync(kFull, over);
-  if (lane == 0) s.sums[warp] = over;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) want -= s.sums[w];
+  want -= sum_cta(over, s.sums);
   if (warp == 0)
     for (int i = 0; i < n && want > 0; i += 32) {
-      const bool is = i + lane < n && keys[i + lane] == same && bits(i + lane) == top;
+      const bool is = i + lane < n && bits(i + lane) == top;
       const unsigned m = __ballot_sync(kFull, is);
       if (is && __popc(m & ((1u << lane) - 1)) < want) atomicOr(&mark[(i + lane) >> 5], 1u << lane);
       want -= __popc(m);
@@ -241,8 +247,8 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
   // attending: ring, joined sums, the queries' operands; selecting: this CTA's scores, everyone's keys
   uint8_t* frag = sm + P::RING + P::JOIN;
   float* join = reinterpret_cast<float*>(sm + P::RING);
-  double* mine = reinterpret_cast<double*>(sm);                                     // [share]
-  int* keys = reinterpret_cast<int*>(mine + share_room);                            // [max_pages]
+  float* mine = reinterpret_cast<float*>(sm);                                       // [share], later as doubles
+  int* keys = reinterpret_cast<int*>(sm + share_room * 8);                          // [max_pages]
   const int body = max(P::ATTEND, share_room * 8 + (a.max_pages * 4 + 7) / 8 * 8);
   unsigned* mark = reinterpret_cast<unsigned*>(sm + body);                          // [max_pages / 32]
   int* list = reinterpret_cast<int*>(mark + (a.max_pages + 31) / 32);               // [top_k] pages, ascending
@@ -297,7 +303,18 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
             for (int k = 0; k < 8; ++k) qs[k] += (double)to_f<T>(x[r][k]);
           }
       }
+      F2 q2[4];
+      float qn = 0.f;                      // the squared norm of all channels
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q2[k] = F2((float)qs[2 * k], (float)qs[2 * k + 1]);
+        const float2 y = q2[k].get();
+        qn = fmaf(y.x, y.x, fmaf(y.y, y.y, qn));
+      }
+#pragma unroll
+      for (int o = 1; o < LPP; o <<= 1) qn += __shfl_xor_sync(kFull, qn, o);
       const uint32_t row = (uint32_t)(row0_of(a, a.layer0 + layer, 0, h) >> a.page_log2);
+      auto mean_at = [&](int p) { return reinterpret_cast<const uint4*>(a.k_mean + (size_t)(row + (uint32_t)p * a.Hkv) * D) + c8; };
       // two steps' pages are on their way while a third's places are looked up
       uint4 w[FLY];
       auto fetch = [&]() {
@@ -306,27 +323,32 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
         for (int f = 0; f < FLY; ++f) {
           const int p = __shfl_sync(kFull, pid, f * PPW + lane / LPP);
           w[f] = make_uint4(0x7fc07fc0u, 0, 0, 0);   // a page that is not there scores NaN
-          if (p >= 0) w[f] = __ldg(reinterpret_cast<const uint4*>(a.k_mean + (size_t)(row + (uint32_t)p * a.Hkv) * D) + c8);
+          if (p >= 0) w[f] = __ldg(mean_at(p));
         }
       };
       fetch();
       pid = ask(c0 + (warp + kWarps) * STEP);
+      float mn2 = 0.f;                     // this lane's channels: the largest squared norm
       for (int base = c0 + warp * STEP; base < c1; base += kWarps * STEP) {
         uint4 now[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) now[f] = w[f];
         fetch();
         pid = ask(base + 2 * kWarps * STEP);
-        double x[FLY];
+        float x[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
           const uint32_t v[4] = {now[f].x, now[f].y, now[f].z, now[f].w};
-          x[f] = 0.0;
+          F2 dot(0.f), norm(0.f);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            x[f] = fma(qs[2 * k], (double)__uint_as_float(v[k] << 16), x[f]);
-            x[f] = fma(qs[2 * k + 1], (double)__uint_as_float(v[k] & 0xffff0000u), x[f]);
+            const F2 m(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xffff0000u));
+            dot = fma2(q2[k], m, dot);
+            norm = fma2(m, m, norm);
           }
+          const float2 d = dot.get(), nn = norm.get();
+          x[f] = d.x + d.y;
+          mn2 = fmaxf(mn2, nn.x + nn.y);   // (NaN, of a page that scores -infinity, plays no part)
         }
         // sums over the LPP lanes of a page: lanes trade halves of their pages, and after three trades a
         // lane holds one page, whose bits its own low bits chose
@@ -339,30 +361,76 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
 #pragma unroll
           for (int f = 0; f < FLY / 2; ++f)
             if (f < have) {
-              const double keep = up ? x[f + have] : x[f], give = up ? x[f] : x[f + have];
+              const float keep = up ? x[f + have] : x[f], give = up ? x[f] : x[f + have];
               x[f] = keep + __shfl_xor_sync(kFull, give, o);
             }
         }
 #pragma unroll
         for (int o = 8; o < LPP; o <<= 1) x[0] += __shfl_xor_sync(kFull, x[0], o);
         const int f = (lane & 1) * 4 + (lane & 2) + (lane >> 2 & 1), c = base + f * PPW + lane / LPP;
-        if (c8 < 8 && c < c1) mine[c - c0] = plain_score(x[0]);
+        if (c8 < 8 && c < c1) mine[c - c0] = x[0] == x[0] ? x[0] : -INFINITY;
       }
+      // A score is the sum over LPP lanes of 4 packed products each, from a sum of queries rounded once: off
+      // by at most 12 roundings of 2^-24 relative to sum |q m| <= |q| |m|, and the square roots' own.
+#pragma unroll
+      for (int o = 16; o >= LPP; o >>= 1) mn2 = fmaxf(mn2, __shfl_xor_sync(kFull, mn2, o));
+#pragma unroll
+      for (int o = 1; o < LPP; o <<= 1) mn2 += __shfl_xor_sync(kFull, mn2, o);
+      if (lane == 0) s.bound[warp] = mn2;
       // 2. everyone's scores, and the best of them
       cluster.sync();
+      float most_n = 0.f;
+      for (int k = lane; k < CS * kWarps; k += 32) most_n = fmaxf(most_n, cluster.map_shared_rank(s.bound, k / kWarps)[k % kWarps]);
+      const float off = 9.5367432e-7f * sqrtf(qn) * sqrtf(warp_max(most_n));   // 2^-20
       int mn = INT_MAX, mx = INT_MIN;
 #pragma unroll 8
       for (int c = tid; c < last; c += kThreads) {
-        const int r = c / share, k = key_of((float)cluster.map_shared_rank(mine, r)[c - r * share]);
+        const int r = c / share, k = key_of(cluster.map_shared_rank(mine, r)[c - r * share]);
         keys[c] = k;
         mn = min(mn, k);
         mx = max(mx, k);
       }
-      select_largest(keys, last, top_k - 1, mn, mx, mark, s, [&](int c) {
-        const int r = c / share;
-        return cluster.map_shared_rank(mine, r)[c - r * share];
+      __syncthreads();
+      // the score of page c in 64 bits, by LPP lanes together
+      auto score64 = [&](int c) {
+        const int p = page_of(a, b, c);
+        double x = NAN;
+        if (p >= 0) {
+          const uint4 m = __ldg(mean_at(p));
+          const uint32_t v[4] = {m.x, m.y, m.z, m.w};
+          x = 0.0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x = fma(qs[2 * k], (double)__uint_as_float(v[k] << 16), x);
+            x = fma(qs[2 * k + 1], (double)__uint_as_float(v[k] & 0xffff0000u), x);
+          }
+        }
+#pragma unroll
+        for (int o = LPP / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        return plain_score(x);
+      };
+      const bool done = select_largest(keys, last, top_k - 1, off, mn, mx, mark, s, [&](int members) {
+        for (int j0 = warp * PPW; j0 < members; j0 += kWarps * PPW) {
+          const int j = min(j0 + lane / LPP, members - 1);
+          const double x = score64(s.list[j]);
+          if (c8 == 0) s.score[j] = x;
+        }
       });
       cluster.sync();                      // `mine` may be overwritten from here on
+      if (!done) {                         // the same in all CTAs: they have the same keys
+        double* all = reinterpret_cast<double*>(sm);
+        for (int c = c0 + warp * PPW; c < c1; c += kWarps * PPW) {
+          const int cc = min(c + lane / LPP, c1 - 1);
+          const double x = score64(cc);
+          if (c8 == 0) all[cc - c0] = x;
+        }
+        cluster.sync();
+        select_exactly(last, top_k - 1, mark, s, [&](int c) {
+          const int r = c / share;
+          return cluster.map_shared_rank(all, r)[c - r * share];
+        });
+        cluster.sync();
+      }
     } else {
       for (int k = tid; k < (last + 31) / 32; k += kThreads) mark[k] = 0;
       __syncthreads();

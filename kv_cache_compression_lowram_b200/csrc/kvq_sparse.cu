@@ -28,6 +28,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 1024;
+constexpr int kDeep = 4;      // stages of mean keys on their way
 constexpr int kRank = 256;    // members of a border bin that are ranked by comparison
 
 template <int BITS, int D, int ROWS, bool F32> struct Plan {
@@ -39,6 +40,8 @@ template <int BITS, int D, int ROWS, bool F32> struct Plan {
   static constexpr int JOIN = kWarps * ROWS * D * 4;
   // what lives at once: the ring and the joined sums, or the scores and the histogram
   static constexpr int ATTEND = RING + JOIN + Tl::QFRAG;
+  // scoring: a ring of mean keys per warp, kDeep stages of 4 x 512 bytes
+  static constexpr int MEANS = kWarps * kDeep * 2048;
   static constexpr int SMALL = Tl::QMETA + kWarps * ROWS * 8 + 2 * ROWS * 4;
   static constexpr int MINB = ATTEND <= 100 * 1024 ? 2 : 1;
 };
@@ -237,7 +240,7 @@ template <class Score> __device__ __noinline__ void select_exactly(int n, int wa
 
 template <int BITS, int D, int ROWS, bool F32>
 __global__ void __launch_bounds__(kThreads, Plan<BITS, D, ROWS, F32>::MINB)
-sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
+sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
               int32_t* __restrict__ sel) {
   using P = Plan<BITS, D, ROWS, F32>;
   using Tl = typename P::Tl;
@@ -247,9 +250,10 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
   // attending: ring, joined sums, the queries' operands; selecting: this CTA's scores, everyone's keys
   uint8_t* frag = sm + P::RING + P::JOIN;
   float* join = reinterpret_cast<float*>(sm + P::RING);
-  float* mine = reinterpret_cast<float*>(sm);                                       // [share], later as doubles
-  int* keys = reinterpret_cast<int*>(sm + share_room * 8);                          // [max_pages]
-  const int body = max(P::ATTEND, share_room * 8 + (a.max_pages * 4 + 7) / 8 * 8);
+  int* keys = reinterpret_cast<int*>(sm);                                           // [max_pages]
+  uint8_t* scores = sm + (a.max_pages * 4 + 15) / 16 * 16;
+  float* mine = reinterpret_cast<float*>(scores);                                   // [share], later as doubles
+  const int body = max(P::ATTEND, score_room);
   unsigned* mark = reinterpret_cast<unsigned*>(sm + body);                          // [max_pages / 32]
   int* list = reinterpret_cast<int*>(mark + (a.max_pages + 31) / 32);               // [top_k] pages, ascending
   float* meta = reinterpret_cast<float*>(list + top_k);
@@ -275,7 +279,7 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
   if (top_k <= last) {
     // 1. scores of the full pages [c0, c1)
     const int share = (last + CS - 1) / CS, c0 = min(rank * share, last), c1 = min(c0 + share, last);
-    constexpr int LPP = D / 8, PPW = 32 / LPP, FLY = 8, STEP = PPW * FLY;   // 32, 16 or 8 pages
+    constexpr int LPP = D / 8, PPW = 32 / LPP, FLY = 4, STEP = PPW * FLY;   // 16, 8 or 4 pages a stage
     const int c8 = lane % LPP;
     if (top_k > 1) {
       auto ask = [&](int base) {
@@ -315,30 +319,34 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
       for (int o = 1; o < LPP; o <<= 1) qn += __shfl_xor_sync(kFull, qn, o);
       const uint32_t row = (uint32_t)(row0_of(a, a.layer0 + layer, 0, h) >> a.page_log2);
       auto mean_at = [&](int p) { return reinterpret_cast<const uint4*>(a.k_mean + (size_t)(row + (uint32_t)p * a.Hkv) * D) + c8; };
-      // two steps' pages are on their way while a third's places are looked up
-      uint4 w[FLY];
-      auto fetch = [&]() {
+      // kDeep - 1 stages are on their way; a lane reads only what it copied itself
+      uint4* ring = reinterpret_cast<uint4*>(scores + (share_room * 4 + 15) / 16 * 16) + (warp * kDeep * FLY) * 32 + lane;
+      int in = 0, rd = 0, next = c0 + (warp + kWarps) * STEP;
+      auto issue = [&]() {
         if (pid == -1) flag(a, KVQ_ERR_PAGE);
+        const int now = pid;
+        pid = ask(next);
+        next += kWarps * STEP;
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
-          const int p = __shfl_sync(kFull, pid, f * PPW + lane / LPP);
-          w[f] = make_uint4(0x7fc07fc0u, 0, 0, 0);   // a page that is not there scores NaN
-          if (p >= 0) w[f] = __ldg(mean_at(p));
+          const int p = __shfl_sync(kFull, now, f * PPW + lane / LPP);
+          uint4* to = ring + (in * FLY + f) * 32;
+          if (p >= 0) cp16(smem_u32(to), mean_at(p));
+          else *to = make_uint4(0x7fc07fc0u, 0, 0, 0);   // a page that is not there scores NaN
         }
+        cp_commit();
+        in = in + 1 == kDeep ? 0 : in + 1;
       };
-      fetch();
-      pid = ask(c0 + (warp + kWarps) * STEP);
+#pragma unroll 1
+      for (int k = 0; k < kDeep - 1; ++k) issue();
       float mn2 = 0.f;                     // this lane's channels: the largest squared norm
       for (int base = c0 + warp * STEP; base < c1; base += kWarps * STEP) {
-        uint4 now[FLY];
-#pragma unroll
-        for (int f = 0; f < FLY; ++f) now[f] = w[f];
-        fetch();
-        pid = ask(base + 2 * kWarps * STEP);
+        cp_wait<kDeep - 2>();
         float x[FLY];
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
-          const uint32_t v[4] = {now[f].x, now[f].y, now[f].z, now[f].w};
+          const uint4 m4 = ring[(rd * FLY + f) * 32];
+          const uint32_t v[4] = {m4.x, m4.y, m4.z, m4.w};
           F2 dot(0.f), norm(0.f);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -350,11 +358,13 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
           x[f] = d.x + d.y;
           mn2 = fmaxf(mn2, nn.x + nn.y);   // (NaN, of a page that scores -infinity, plays no part)
         }
-        // sums over the LPP lanes of a page: lanes trade halves of their pages, and after three trades a
-        // lane holds one page, whose bits its own low bits chose
+        rd = rd + 1 == kDeep ? 0 : rd + 1;
+        issue();
+        // sums over the LPP lanes of a page: lanes trade halves of their pages, and after two trades a lane
+        // holds one page, whose bits its own low bits chose
         int have = FLY;
 #pragma unroll
-        for (int t = 0; t < 3; ++t) {
+        for (int t = 0; t < 2; ++t) {
           have >>= 1;
           const int o = 1 << t;
           const bool up = lane & o;
@@ -366,10 +376,11 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
             }
         }
 #pragma unroll
-        for (int o = 8; o < LPP; o <<= 1) x[0] += __shfl_xor_sync(kFull, x[0], o);
-        const int f = (lane & 1) * 4 + (lane & 2) + (lane >> 2 & 1), c = base + f * PPW + lane / LPP;
-        if (c8 < 8 && c < c1) mine[c - c0] = x[0] == x[0] ? x[0] : -INFINITY;
+        for (int o = 4; o < LPP; o <<= 1) x[0] += __shfl_xor_sync(kFull, x[0], o);
+        const int f = (lane & 1) * 2 + (lane >> 1 & 1), c = base + f * PPW + lane / LPP;
+        if (c8 < 4 && c < c1) mine[c - c0] = x[0] == x[0] ? x[0] : -INFINITY;
       }
+      cp_wait<0>();
       // A score is the sum over LPP lanes of 4 packed products each, from a sum of queries rounded once: off
       // by at most 12 roundings of 2^-24 relative to sum |q m| <= |q| |m|, and the square roots' own.
 #pragma unroll
@@ -418,7 +429,7 @@ sparse_kernel(Args a, int top_k, int share_room, const void* __restrict__ qv, co
       });
       cluster.sync();                      // `mine` may be overwritten from here on
       if (!done) {                         // the same in all CTAs: they have the same keys
-        double* all = reinterpret_cast<double*>(sm);
+        double* all = reinterpret_cast<double*>(scores);
         for (int c = c0 + warp * PPW; c < c1; c += kWarps * PPW) {
           const int cc = min(c + lane / LPP, c1 - 1);
           const double x = score64(cc);
@@ -612,9 +623,12 @@ cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, voi
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   auto share_room = [&](int cs) { return (a.max_pages + cs - 1) / cs; };
+  auto score_room = [&](int cs) {   // all keys, then a share's scores in fp32 and the ring, or its scores in fp64
+    const int fast = (share_room(cs) * 4 + 15) / 16 * 16 + P::MEANS, exact = share_room(cs) * 8;
+    return (a.max_pages * 4 + 15) / 16 * 16 + (fast > exact ? fast : exact);
+  };
   auto smem_of = [&](int cs) {
-    const int scores = share_room(cs) * 8 + (a.max_pages * 4 + 7) / 8 * 8;
-    return (scores > P::ATTEND ? scores : P::ATTEND) + (a.max_pages + 31) / 32 * 4 + top_k * 4 + P::SMALL + 16;
+    return (score_room(cs) > P::ATTEND ? score_room(cs) : P::ATTEND) + (a.max_pages + 31) / 32 * 4 + top_k * 4 + P::SMALL + 16;
   };
   int now[4];
   int* fit = dev < 64 ? fits[dev] : now;
@@ -646,7 +660,7 @@ cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, voi
   cfg.gridDim = units * cs;
   attr.val.clusterDim.x = cs;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, top_k, share_room(cs), q, lens, out, sel);
+  return cudaLaunchKernelEx(&cfg, kernel, a, top_k, share_room(cs), score_room(cs), q, lens, out, sel);
 }
 
 template <int BITS, bool F32>

@@ -17,6 +17,7 @@ The quantised KV cache (``lowram_kvq_write``, ``lowram_kvq_read``, ``lowram_kvq_
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -737,24 +738,50 @@ def _kvq_dtype(c):
 _I64x4 = ctypes.c_int64 * 4
 
 
-def _kvq_rows(c, t, name, n_layers=None, n=None):
-    """(pointer, strides) of a [n_layers][B][n][Hkv][d] tensor with contiguous rows."""
-    shape = t.shape
-    if len(shape) != 5 or shape[1:4:2] != (c.batch, c.n_kv_heads) or shape[4] != c.head_dim \
-            or (n is not None and (shape[0] != n_layers or shape[2] != n)):
+@functools.lru_cache(maxsize=256)
+def _kvq_strides(s):
+    """The first four of five strides as a C array (one per distinct tuple; the library only reads it)."""
+    return _I64x4(*s[:4])
+
+
+def _kvq_rows(dims, t, name, n_layers=None, n=None):
+    """(pointer, strides, n_layers, tokens) of a [n_layers][B][n][Hkv][d] tensor with contiguous rows."""
+    try:
+        layers, batch, tokens, heads, d = t.shape
+    except ValueError:
+        layers = batch = tokens = heads = d = -1
+    if batch != dims[0] or heads != dims[1] or d != dims[3] or (n is not None and (layers != n_layers or tokens != n)):
         raise ValueError(f"{name} must be [n_layers][batch][tokens][n_kv_heads][head_dim]")
     s = t.stride()
-    if not t.is_cuda or t.dtype != _kvq_dtype(c) or s[4] != 1:
+    if s[4] != 1 or t.dtype is not dims[4] or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of the cache's dtype with contiguous rows")
-    return t.data_ptr(), _I64x4(s[0], s[1], s[2], s[3])
+    return t.data_ptr(), _kvq_strides(s), layers, tokens
 
 
-def _kvq_ints(c, t, name, device):
+def _kvq_ints(dims, t, name, device):
     if t is None:
         return None
-    if t.shape != (c.batch,) or t.dtype != _kvq_torch()[0].int32 or t.device != device or not t.is_contiguous():
+    if t.dtype is not dims[5] or t.shape != dims[6] or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [batch] tensor on the device of the data")
     return t.data_ptr()
+
+
+def _kvq_prepared(cfg, arrays):
+    """(C config, C cache, dims): dims = (B, Hkv, Hq, d, dtype, int32, (B,)) as the checks use them."""
+    if isinstance(cfg, _KvqPrepared):
+        return cfg
+    return _KvqPrepared(kvq_config_struct(cfg), arrays)
+
+
+class _KvqPrepared:
+    """A config and its arrays after their checks, with what a call passes on."""
+
+    def __init__(self, c, arrays):
+        torch = _kvq_torch()[0]
+        self.config, self.cache = c, _kvq_cache_struct(c, arrays)
+        self.c, self.k = ctypes.byref(self.config), ctypes.byref(self.cache)
+        self.dims = (c.batch, c.n_kv_heads, c.n_q_heads, c.head_dim, torch.float32 if c.dtype == 0 else torch.bfloat16,
+                     torch.int32, (c.batch,))
 
 
 def lowram_kvq_token_bytes(cfg) -> int:
@@ -771,67 +798,68 @@ def lowram_kvq_workspace_bytes(cfg, n_layers: int, n_q: int) -> int:
 def lowram_kvq_write(cfg, arrays, layer0: int, k, v, pos, count=None, stream=None) -> None:
     """Quantise k, v [n_layers][B][n][Hkv][d] (any strides with contiguous, 16-byte aligned rows)
     into the cache arrays from slot pos[b] on; count[b] of the n tokens, or all (see lowram.h)."""
-    c = kvq_config_struct(cfg)
-    src = _kvq_cache_struct(c, arrays)
-    kp, ks = _kvq_rows(c, k, "k")
-    vp, vs = _kvq_rows(c, v, "v", k.shape[0], k.shape[2])
-    if v.device != k.device:
+    p = _kvq_prepared(cfg, arrays)
+    kp, ks, layers, n = _kvq_rows(p.dims, k, "k")
+    vp, vs, _, _ = _kvq_rows(p.dims, v, "v", layers, n)
+    dev = k.device
+    if v.device != dev:
         raise ValueError("k and v must be on one device")
-    dev, shape = k.device, k.shape
-    _kvq_call(lib().lowram_kvq_write, "lowram_kvq_write", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
-              shape[0], shape[2], kp, ks, vp, vs, _kvq_ints(c, pos, "pos", dev), _kvq_ints(c, count, "count", dev))
+    _kvq_call(lib().lowram_kvq_write, "lowram_kvq_write", dev, stream, p.c, p.k, layer0, layers, n, kp, ks, vp, vs,
+              _kvq_ints(p.dims, pos, "pos", dev), _kvq_ints(p.dims, count, "count", dev))
 
 
 def lowram_kvq_read(cfg, arrays, layer0: int, k_out, v_out, pos, count=None, stream=None) -> None:
     """Read tokens pos[b] + i, i < count[b] (or all), into k_out, v_out [n_layers][B][n][Hkv][d]."""
-    c = kvq_config_struct(cfg)
-    src = _kvq_cache_struct(c, arrays)
-    kp, ks = _kvq_rows(c, k_out, "k_out")
-    vp, vs = _kvq_rows(c, v_out, "v_out", k_out.shape[0], k_out.shape[2])
-    if v_out.device != k_out.device:
+    p = _kvq_prepared(cfg, arrays)
+    kp, ks, layers, n = _kvq_rows(p.dims, k_out, "k_out")
+    vp, vs, _, _ = _kvq_rows(p.dims, v_out, "v_out", layers, n)
+    dev = k_out.device
+    if v_out.device != dev:
         raise ValueError("k_out and v_out must be on one device")
-    dev, shape = k_out.device, k_out.shape
-    _kvq_call(lib().lowram_kvq_read, "lowram_kvq_read", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
-              shape[0], shape[2], kp, ks, vp, vs, _kvq_ints(c, pos, "pos", dev), _kvq_ints(c, count, "count", dev))
+    _kvq_call(lib().lowram_kvq_read, "lowram_kvq_read", dev, stream, p.c, p.k, layer0, layers, n, kp, ks, vp, vs,
+              _kvq_ints(p.dims, pos, "pos", dev), _kvq_ints(p.dims, count, "count", dev))
 
 
-def _kvq_queries(c, q, out):
+def _kvq_queries(dims, q, out):
     shape = q.shape
-    if len(shape) != 5 or shape[1:4:2] != (c.batch, c.n_q_heads) or shape[4] != c.head_dim:
+    try:
+        layers, batch, n, heads, d = shape
+    except ValueError:
+        layers = batch = n = heads = d = -1
+    if batch != dims[0] or heads != dims[2] or d != dims[3]:
         raise ValueError("q must be [n_layers][batch][n_q][n_q_heads][head_dim]")
-    if out.shape != shape or out.dtype != q.dtype or out.device != q.device:
-        raise ValueError("out must be like q")
-    if not q.is_cuda or q.dtype != _kvq_dtype(c):
+    if q.dtype is not dims[4] or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor of the cache's dtype")
-    return _ptr(q), _ptr(out), shape
+    if out.shape != shape or out.dtype is not dims[4] or out.device != q.device:
+        raise ValueError("out must be like q")
+    if not (q.is_contiguous() and out.is_contiguous()):
+        raise ValueError("tensors passed to liblowram must be contiguous")
+    return q.data_ptr(), out.data_ptr(), layers, n
 
 
 def lowram_kvq_decode_attn(cfg, arrays, layer0: int, q, lens, out, workspace, stream=None) -> None:
     """Attention of q [n_layers][B][n_q][Hq][d] (each sequence's last n_q tokens) over whole
     sequences of lens[b] tokens.  ``workspace``: lowram_kvq_workspace_bytes bytes, zeroed once."""
-    c = kvq_config_struct(cfg)
-    src = _kvq_cache_struct(c, arrays)
-    qp, op, shape = _kvq_queries(c, q, out)
+    p = _kvq_prepared(cfg, arrays)
+    qp, op, layers, n = _kvq_queries(p.dims, q, out)
     dev = q.device
     if workspace.device != dev:
         raise ValueError("workspace must be on the device of q")
-    _kvq_call(lib().lowram_kvq_decode_attn, "lowram_kvq_decode_attn", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
-              shape[0], shape[2], qp, _kvq_ints(c, lens, "lens", dev), op, _ptr(workspace),
-              workspace.numel() * workspace.element_size())
+    _kvq_call(lib().lowram_kvq_decode_attn, "lowram_kvq_decode_attn", dev, stream, p.c, p.k, layer0, layers, n, qp,
+              _kvq_ints(p.dims, lens, "lens", dev), op, _ptr(workspace), workspace.numel() * workspace.element_size())
 
 
 def lowram_kvq_sparse_attn(cfg, arrays, layer0: int, top_k: int, q, lens, out, sel=None, stream=None) -> None:
     """The same over each query's newest page and its top_k - 1 best older pages; ``sel``
     [n_layers][B][n_q][Hkv][top_k] int32 takes their places in the sequence (then -1)."""
-    c = kvq_config_struct(cfg)
-    src = _kvq_cache_struct(c, arrays)
-    qp, op, shape = _kvq_queries(c, q, out)
+    p = _kvq_prepared(cfg, arrays)
+    qp, op, layers, n = _kvq_queries(p.dims, q, out)
     dev = q.device
-    if sel is not None and (tuple(sel.shape) != tuple(shape[:3]) + (c.n_kv_heads, top_k)
-                            or sel.dtype != _kvq_torch()[0].int32 or sel.device != dev):
+    if sel is not None and (tuple(sel.shape) != (layers, p.dims[0], n, p.dims[1], top_k) or sel.dtype is not p.dims[5]
+                            or sel.device != dev):
         raise ValueError("sel must be int32 [n_layers][batch][n_q][n_kv_heads][top_k] on the device of q")
-    _kvq_call(lib().lowram_kvq_sparse_attn, "lowram_kvq_sparse_attn", dev, stream, ctypes.byref(c), ctypes.byref(src), layer0,
-              shape[0], shape[2], top_k, qp, _kvq_ints(c, lens, "lens", dev), op, _ptr(sel))
+    _kvq_call(lib().lowram_kvq_sparse_attn, "lowram_kvq_sparse_attn", dev, stream, p.c, p.k, layer0, layers, n, top_k, qp,
+              _kvq_ints(p.dims, lens, "lens", dev), op, _ptr(sel))
 
 
 class LowramKvq:
@@ -853,11 +881,11 @@ class LowramKvq:
             arrays["table"] = table
         get = lambda n: arrays.get(n) if isinstance(arrays, dict) else getattr(arrays, n, None)  # noqa: E731
         self.arrays = {n: get(n) for n in _kvq_layouts(c)}
-        self._cache = _kvq_cache_struct(c, self.arrays)
+        self._calls = _KvqPrepared(c, self.arrays)
         self.device = dev = self.arrays["k_code"].device
         if self.arrays["err"] is None:
             self.arrays["err"] = torch.zeros(1, dtype=torch.int32, device=dev)
-            self._cache.err = self.arrays["err"].data_ptr()
+            self._calls.cache.err = self.arrays["err"].data_ptr()
         self._workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
         torch.cuda.current_stream(dev).synchronize()   # ready for whichever stream comes first
 
@@ -868,7 +896,7 @@ class LowramKvq:
     def write(self, k, v, pos, count=None, layer0: int = 0, stream=None) -> None:
         """Quantise k, v [n_layers][B][n][Hkv][d] into slots pos[b] .. pos[b] + count[b] - 1."""
         self._mine(k)
-        lowram_kvq_write(self.config, self._cache, layer0, k, v, pos, count, stream)
+        lowram_kvq_write(self._calls, None, layer0, k, v, pos, count, stream)
 
     def read(self, pos, count=None, n: Optional[int] = None, layer0: int = 0, n_layers: Optional[int] = None, out=None,
              stream=None):
@@ -880,7 +908,7 @@ class LowramKvq:
             shape = (c.n_layers - layer0 if n_layers is None else n_layers, c.batch, n, c.n_kv_heads, c.head_dim)
             out = tuple(torch.zeros(shape, dtype=_kvq_dtype(c), device=self.device) for _ in range(2))
         self._mine(out[0])
-        lowram_kvq_read(self.config, self._cache, layer0, out[0], out[1], pos, count, stream)
+        lowram_kvq_read(self._calls, None, layer0, out[0], out[1], pos, count, stream)
         return out
 
     def decode(self, q, lens, out=None, layer0: int = 0, stream=None):
@@ -888,7 +916,7 @@ class LowramKvq:
         self._mine(q)
         if out is None:
             out = _kvq_torch()[0].empty_like(q)
-        lowram_kvq_decode_attn(self.config, self._cache, layer0, q, lens, out, self._workspace, stream)
+        lowram_kvq_decode_attn(self._calls, None, layer0, q, lens, out, self._workspace, stream)
         return out
 
     def decode_sparse(self, q, lens, top_k: int, out=None, sel: bool = False, layer0: int = 0, stream=None):
@@ -899,7 +927,7 @@ class LowramKvq:
             out = torch.empty_like(q)
         s = torch.empty(tuple(q.shape[:3]) + (self.config.n_kv_heads, top_k), dtype=torch.int32,
                         device=q.device) if sel else None
-        lowram_kvq_sparse_attn(self.config, self._cache, layer0, top_k, q, lens, out, s, stream)
+        lowram_kvq_sparse_attn(self._calls, None, layer0, top_k, q, lens, out, s, stream)
         return (out, s) if sel else out
 
     def validate(self) -> int:

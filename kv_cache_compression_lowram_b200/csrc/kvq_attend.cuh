@@ -12,7 +12,8 @@
 // every code would first have to be stored as 16 bits.
 //
 // Scores.  x_t = sum_g s_tg (n_tg . q_g) + lo_tg sum(q_g): the scale and the offset of a group enter
-// per accumulator, in fp32, so keys are never rounded.  q is multiplied by a power of two per
+// per accumulator, in fp32, so keys are never rounded.  (fp32 calls
+// unpack to centred codes, and lose nothing to sums that cancel either.)  q is multiplied by a power of two per
 // row so that its largest entry lies in [2^13, 2^14): bf16 values stay exact in fp16 down to
 // 2^-27 of the largest (an fp32 q is split into two fp16 parts).
 //
@@ -96,32 +97,38 @@ template <int BYTES> __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4
   }
 }
 
-// The two 16-bit lanes of half j (0, 1) of a cell: even codes in `a`, odd ones in `b` (4 bits: 16
-// times too large, made up for in B or in the output).
-template <int BITS>
-__device__ __forceinline__ void half_cell(const uint32_t* w, int j, uint32_t& a, uint32_t& b) {
-  if constexpr (BITS == 4) {
-    const uint32_t x = j ? w[0] >> 8 : w[0];
-    a = x & 0x000F000Fu;
-    b = x & 0x00F000F0u;
+// Codes in 16-bit lanes as they are (n 2^-24, or n 2^-20 where HIGH), or centred for fp32 calls:
+// n - 2^(b-1), or 16 times that, by way of 1024 + n in fp16.
+template <int BITS, bool CENTRE, bool HIGH> __device__ __forceinline__ uint32_t lanes(uint32_t x) {
+  constexpr uint32_t kMask = BITS == 8 ? 0x00FF00FFu : (HIGH ? 0x00F000F0u : 0x000F000Fu);
+  if constexpr (!CENTRE) {
+    return x & kMask;
   } else {
-    a = w[j] & 0x00FF00FFu;
-    b = (w[j] >> 8) & 0x00FF00FFu;
+    const uint32_t y = (x & kMask) | 0x64006400u, c = BITS == 4 && !HIGH ? 0x64086408u : 0x64806480u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
+// The two 16-bit lanes of half j (0, 1) of a cell: even codes in `a`, odd ones in `b` (4 bits: 16
+// times too large, made up for in B or in the output).
+template <int BITS, bool CENTRE>
+__device__ __forceinline__ void half_cell(const uint32_t* w, int j, uint32_t& a, uint32_t& b) {
+  const uint32_t x = BITS == 4 ? (j ? w[0] >> 8 : w[0]) : w[BITS == 4 ? 0 : j];
+  a = lanes<BITS, CENTRE, false>(x);
+  b = lanes<BITS, CENTRE, true>(BITS == 4 ? x : x >> 8);
+}
 // Codes 2j, 2j + 1 of a cell of two tokens (low lanes: the first token).
-template <int BITS>
+template <int BITS, bool CENTRE>
 __device__ __forceinline__ void pair_cell(const uint32_t* w0, const uint32_t* w1, int j, uint32_t& a, uint32_t& b) {
+  uint32_t x;
   if constexpr (BITS == 4) {
-    uint32_t x = __byte_perm(w0[0], w1[0], j < 2 ? 0x5410 : 0x7632);
+    x = __byte_perm(w0[0], w1[0], j < 2 ? 0x5410 : 0x7632);
     if (j & 1) x >>= 8;
-    a = x & 0x000F000Fu;
-    b = x & 0x00F000F0u;
   } else {
-    const uint32_t x = __byte_perm(w0[j / 2], w1[j / 2], j & 1 ? 0x7632 : 0x5410);
-    a = x & 0x00FF00FFu;
-    b = (x >> 8) & 0x00FF00FFu;
+    x = __byte_perm(w0[j / 2], w1[j / 2], j & 1 ? 0x7632 : 0x5410);
   }
+  a = lanes<BITS, CENTRE, false>(x);
+  b = lanes<BITS, CENTRE, true>(BITS == 4 ? x : x >> 8);
 }
 
 template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
@@ -144,6 +151,8 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // fp16's smallest step (2^-24) loses is 2^-30 (fp32: 2^-34) of a weight of one.
   static constexpr float kSlack = F32 ? 2.f : 4.f, kWide = F32 ? 8.f : 16.f, kBias = F32 ? 1024.f : 64.f;
 
+  // What a code is multiplied by to be a number: fp32 calls centre their codes and have the 1.
+  static constexpr float kCode = F32 ? 1.f : 16777216.f;
   // Codes are summed as n - kMid, so that an average over many tokens is not a small difference of
   // two large sums; the offsets become lo + kMid s.  kMidLow, kMidHigh: -kMid as two fp16 lanes, in
   // the units of the codes of rows r and r + 8.
@@ -208,8 +217,8 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         const float sigma = e > -127 && e < 128 ? __uint_as_float((unsigned)(min(13 - e, 100) + 127) << 23) : 1.f;
 #pragma unroll
         for (int i = 16 / G; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);   // 32 / G lanes hold a group
-        if (lane == 0) meta[j] = kLog2e * rsqrtf((float)D) * (16777216.f / sigma);
-        if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * sigma * (1.f / 16777216.f);
+        if (lane == 0) meta[j] = kLog2e * rsqrtf((float)D) * (kCode / sigma);
+        if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * sigma * (1.f / kCode);
         const int col = CP == 1 ? 2 * j : j % 8, tile = CP == 1 ? 0 : j / 8;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -318,8 +327,8 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t a0, a1, a2, a3;
-            half_cell<BITS>(k0 + (e * G + g) * CW, h, a0, a2);
-            half_cell<BITS>(k1 + (e * G + g) * CW, h, a1, a3);
+            half_cell<BITS, F32>(k0 + (e * G + g) * CW, h, a0, a2);
+            half_cell<BITS, F32>(k1 + (e * G + g) * CW, h, a1, a3);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -329,8 +338,12 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
           acc[0][0] += acc[0][1];
           acc[0][2] += acc[0][3];
         }
-        const float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&m0[g]));
-        const float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&m1[g]));
+        float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&m0[g]));
+        float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&m1[g]));
+        if constexpr (F32) {
+          u0.y = fmaf(kMid, u0.x, u0.y);
+          u1.y = fmaf(kMid, u1.x, u1.y);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -402,7 +415,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
     for (int gs = 0; gs < SETS; ++gs) {
       uint2 w[N][NT][SP];
-      float base[NT][4];   // -kMid sum_t w_t in every row: the products below then add w (n - kMid)
+      float base[NT][4];   // -kMid sum_t w_t in every row: the products below then add w (n - kMid) (fp32: 0)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -446,8 +459,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
           } else {
             w[b][t][0] = make_uint2(trans8x8(pack_h2(y[0][0], y[0][1])), trans8x8(pack_h2(y[1][0], y[1][1])));
           }
-#pragma unroll
-          for (int i = SP - 1; i >= 0; --i) mma_f16(base[t], kMidLow, kMidHigh, kMidLow, kMidHigh, w[b][t][i]);
+          if constexpr (!F32) mma_f16(base[t], kMidLow, kMidHigh, kMidLow, kMidHigh, w[b][t][0]);
         }
       }
 #pragma unroll
@@ -464,8 +476,8 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
           for (int b = 0; b < N; ++b) {
             uint32_t a0, a1, a2, a3;
-            pair_cell<BITS>(v[b][0] + g * CW, v[b][1] + g * CW, j, a0, a1);
-            pair_cell<BITS>(v[b][2] + g * CW, v[b][3] + g * CW, j, a2, a3);
+            pair_cell<BITS, F32>(v[b][0] + g * CW, v[b][1] + g * CW, j, a0, a1);
+            pair_cell<BITS, F32>(v[b][2] + g * CW, v[b][3] + g * CW, j, a2, a3);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -556,7 +568,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // The unnormalised outputs [ROWS][D], times weight(row) (0: left out; its sums may be anything).
   template <class Weight> __device__ __forceinline__ void store_out(float* to, Weight weight) const {
     const int r = (threadIdx.x & 31) >> 2;
-    const float u0 = unit_inv == 0.f ? 0.f : 16777216.f / unit_inv, u1 = BITS == 4 ? u0 * 0.0625f : u0;
+    const float u0 = unit_inv == 0.f ? 0.f : kCode / unit_inv, u1 = BITS == 4 ? u0 * 0.0625f : u0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll

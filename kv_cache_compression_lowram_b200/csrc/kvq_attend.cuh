@@ -98,14 +98,16 @@ template <int BYTES> __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4
 }
 
 // Codes in 16-bit lanes as they are (n 2^-24, or n 2^-20 where HIGH), or centred for fp32 calls:
-// n - 2^(b-1), or 16 times that, by way of 1024 + n in fp16.
+// n - (2^b - 1) / 2, or 16 times that, by way of 1024 + n in fp16 (all steps exact).
 template <int BITS, bool CENTRE, bool HIGH> __device__ __forceinline__ uint32_t lanes(uint32_t x) {
   constexpr uint32_t kMask = BITS == 8 ? 0x00FF00FFu : (HIGH ? 0x00F000F0u : 0x000F000Fu);
   if constexpr (!CENTRE) {
     return x & kMask;
   } else {
     const uint32_t y = (x & kMask) | 0x64006400u, c = BITS == 4 && !HIGH ? 0x64086408u : 0x64806480u;
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&c));
+    const uint32_t half = BITS == 4 && HIGH ? 0x48004800u : 0x38003800u;   // 8 or 0.5
+    const __half2 h = __hadd2(__hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&c)),
+                              *reinterpret_cast<const __half2*>(&half));
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
@@ -156,7 +158,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // Codes are summed as n - kMid, so that an average over many tokens is not a small difference of
   // two large sums; the offsets become lo + kMid s.  kMidLow, kMidHigh: -kMid as two fp16 lanes, in
   // the units of the codes of rows r and r + 8.
-  static constexpr float kMid = BITS == 4 ? 8.f : 128.f;
+  static constexpr float kMid = (BITS == 4 ? 8.f : 128.f) - (F32 ? 0.5f : 0.f);
   static constexpr uint32_t kMidLow = BITS == 4 ? 0x80088008u : 0x80808080u, kMidHigh = 0x80808080u;
 
   // [..][i * CP + c]: A's row r + 8 i, the lane's c-th column

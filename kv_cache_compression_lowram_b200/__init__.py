@@ -903,6 +903,8 @@ class LowramKvq:
         """(k, v) [n_layers][B][n][Hkv][d] of tokens pos[b] + i; rows behind count[b] are left as
         they are in ``out`` (zero without it)."""
         if out is None:
+            if stream is not None or n is None:
+                raise ValueError("read needs out, or n and the current stream")
             torch = _kvq_torch()[0]
             c = self.config
             shape = (c.n_layers - layer0 if n_layers is None else n_layers, c.batch, n, c.n_kv_heads, c.head_dim)

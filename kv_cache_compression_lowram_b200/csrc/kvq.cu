@@ -86,11 +86,11 @@ lowram_status rows_call(bool writes, const lowram_kvq_config* cfg, const lowram_
   lowram_status st = check_cache(cfg, cache, layer0, n_layers, &a);
   if (st != LOWRAM_OK) return st;
   if (n < 0 || n > (a.max_pages << a.page_log2)) return inval("the token count must lie in [0, max_pages * page]");
+  if (n == 0) return LOWRAM_OK;
   a.n = n;
   if (!pos) return inval("pos is NULL");
   if ((st = check_rows(a, cfg->dtype, k, ks, !writes, &rk)) != LOWRAM_OK) return st;
   if ((st = check_rows(a, cfg->dtype, v, vs, !writes, &rv)) != LOWRAM_OK) return st;
-  if (n == 0) return LOWRAM_OK;
   const long long pieces = ((n - 1) >> a.page_log2) + 2;
   if (pieces * a.n_layers * a.B * a.Hkv >= (1LL << 31)) return inval("too many rows for one call: split the layers");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -394,7 +394,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < 2 * CP; ++k) high |= x[b][t][k] > thr[t][k % CP];
-    if (__any_sync(kFull, high)) move<N>(x, most_s & 0xffffu);
+    if (__any_sync(kFull, high)) move<N>(x, vm);
     // weights: p in x's place, the sum of the weights
 #pragma unroll
     for (int b = 0; b < N; ++b)
@@ -499,11 +499,21 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // A score passed the running maximum, or a value scale its unit's room: both anew.  A unit that
   // has become far too large is made smaller here as well: the scales it was made for have lost
   // their weight only if the maximum has moved.
-  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][2 * CP], uint32_t most_s) {
-    const uint32_t sb = __reduce_max_sync(kFull, most_s);
+  template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][2 * CP], const uint32_t (&vm)[TB][2][G]) {
+    uint32_t sb = 0;   // the largest finite scale (one that is not spoils the rows that see it, but not the unit)
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint32_t s16 = vm[b][i][g] & 0xffffu;
+          sb = max(sb, s16 < 0x7c00u ? s16 : 0u);
+        }
+    sb = __reduce_max_sync(kFull, sb);
     const float s = __half2float(__ushort_as_half((unsigned short)sb));
     float scale = 1.f;
-    if (sb && sb < 0x7c00u && (unit_inv == 0.f || sb > top_s || !(s * unit_inv > kBias / kWide))) {
+    if (sb && (unit_inv == 0.f || sb > top_s || !(s * unit_inv > kBias / kWide))) {
       const float inv = kBias * __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);   // kBias <= s inv < 2 kBias
       scale = unit_inv == 0.f ? 1.f : inv / unit_inv;
       unit_inv = inv;

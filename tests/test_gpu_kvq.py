@@ -297,6 +297,113 @@ def test_sparse_many_pages(batch, heads, ctx, page, top_k):
     check_attention(cfg, arrays, q, lens, out, top_k=top_k, sel=sel)
 
 
+def test_decode_many_short_and_one_long():
+    """More sequences than a warp has lanes, nearly all empty or of a few tokens."""
+    lens = [0, 1, 2, 5, 33] * 8 + [700] + [3] * 30
+    cfg = config(batch=len(lens), kv_heads=1, q_heads=4, page=16, max_pages=44, n_pages=50)
+    arrays = fill(dict(cfg, batch=1, max_pages=1), 20)
+    arrays["table"] = np.random.default_rng(6).integers(0, 50, (len(lens), 44)).astype(np.int32)
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    q = queries(cfg)
+    check_attention(cfg, arrays, q, lens, cache.decode(q.to(DEV), i32(lens)))
+    out, sel = cache.decode_sparse(q.to(DEV), i32(lens), 6, sel=True)
+    check_attention(cfg, arrays, q, lens, out, top_k=6, sel=sel)
+
+
+def test_calls_of_several_kinds_share_a_workspace():
+    """Layers, query tokens and lengths change from call to call; the counters end at zero each time."""
+    cfg = config(batch=3, layers=3, kv_heads=2, q_heads=6, page=32, max_pages=200, n_pages=210)
+    arrays = fill(dict(cfg, batch=1, max_pages=1), 21)
+    arrays["table"] = np.random.default_rng(8).integers(0, 210, (3, 200)).astype(np.int32)
+    cache = K.LowramKvq(cfg, to_device(arrays), max_q=5)
+    for n, layers, lens in ((5, 3, [6400, 3000, 17]), (1, 1, [6400, 1, 0]), (2, 2, [600, 5000, 6000]), (5, 1, [6400, 6400, 6400]), (1, 3, [90, 80, 70])):
+        q = queries(cfg, n, layers, seed=n + layers)
+        check_attention(cfg, arrays, q, lens, cache.decode(q.to(DEV), i32(lens)))
+    assert not cache._workspace[-4 * 3 * 3 * 2 * 2:].any()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_nan_in_a_token_that_an_earlier_query_does_not_see(bits):
+    cfg = config(batch=1, kv_heads=1, q_heads=4, page=16, max_pages=4, bits=bits)
+    arrays = fill(cfg, 22)
+    p = arrays["table"][0, 39 // 16]
+    for x in "kv":
+        arrays[x + "_scale"][0, p, 0, 39 % 16] = np.float16(np.nan)
+    cache = K.LowramKvq(cfg, to_device(arrays), max_q=3)
+    q = queries(cfg, 3)
+    for out in (cache.decode(q.to(DEV), i32([40])), cache.decode_sparse(q.to(DEV), i32([40]), 4)):
+        assert torch.isnan(out[0, 0, 2]).all()
+        arrays["k_scale"][0, p, 0, 39 % 16] = arrays["v_scale"][0, p, 0, 39 % 16] = 0      # for the oracle: not seen
+        check_attention(cfg, arrays, q[:, :, :2], [39], out[:, :, :2].contiguous())
+        arrays["k_scale"][0, p, 0, 39 % 16] = arrays["v_scale"][0, p, 0, 39 % 16] = np.float16(np.nan)
+
+
+def test_refusals_on_the_device():
+    cfg = config(batch=2, kv_heads=2, q_heads=4)
+    cache = K.LowramKvq(cfg, to_device(fill(cfg, 23)))
+    q, lens = queries(cfg).to(DEV), i32([20, 30])
+    odd = torch.empty(q.numel() + 1, dtype=q.dtype, device=DEV)[1:].view(q.shape)
+    x = torch.zeros(1, 2, 3, 2, 128, dtype=torch.bfloat16, device=DEV)
+    wide = torch.zeros(1, 2, 3, 2, 130, dtype=torch.bfloat16, device=DEV)[..., :128]
+    for call in (lambda: cache.decode(odd, lens), lambda: cache.decode(q, lens, out=odd), lambda: cache.decode_sparse(odd, lens, 2),
+                 lambda: cache.write(wide, x, lens), lambda: cache.decode(q, lens, layer0=1), lambda: cache.decode_sparse(q, lens, 0),
+                 lambda: cache.read(lens, out=(x, x[:, :, :1].expand_as(x))),
+                 lambda: cache.decode(torch.zeros(1, 2, 2, 4, 128, dtype=q.dtype, device=DEV), lens, out=None, layer0=-1)):
+        with pytest.raises(K.LowramError) as ei:
+            call()
+        assert ei.value.status == 1
+    for call in (lambda: cache.decode(q, lens.long()), lambda: cache.decode(q, lens[:1]), lambda: cache.decode(q.float(), lens),
+                 lambda: cache.decode(q, lens.cpu()), lambda: cache.decode(q.transpose(2, 3), lens), lambda: cache.write(x, x, None and lens, lens.cpu()),
+                 lambda: cache.read(lens, n=None), lambda: cache.read(lens, n=3, stream=torch.cuda.Stream())):
+        with pytest.raises((ValueError, K.LowramError)):
+            call()
+    none = torch.zeros(1, 2, 0, 2, 128, dtype=torch.bfloat16, device=DEV)
+    cache.write(none, none, lens)      # nothing to do is not an error
+    few = K.LowramKvq(cfg, cache.arrays, max_q=1)
+    assert few.validate() == 0
+
+
+@pytest.mark.parametrize("kind", ["equal", "two_values", "last_bits"])
+@pytest.mark.parametrize("heads", [1, 40])
+def test_sparse_scores_too_near_for_fp32(kind, heads):
+    """More pages near the border than are ranked by comparison: equal means, two values, and means whose
+    scores differ in the last bits of 64 only."""
+    pages = 700
+    cfg = config(batch=1, kv_heads=heads, q_heads=heads, head_dim=64, page=16, max_pages=pages, n_pages=pages)
+    arrays = fill(dict(cfg, n_pages=2, max_pages=1), 24)
+    arrays = {n: (np.repeat(v[:, :1], pages, 1) if n != "table" else np.arange(pages, dtype=np.int32)[None]) for n, v in arrays.items()}
+    r = np.random.default_rng(9)
+    m = arrays["k_mean"]
+    m[:] = 0
+    m[..., 0] = 1.0
+    if kind == "two_values":
+        m[0, r.permutation(pages)[:300], :, 0] = 1.5
+    if kind == "last_bits":      # a channel whose product is 2^-40 of the score
+        m[..., 1] = r.integers(0, 200, (1, pages, 1))
+    q = torch.ones(1, 1, 1, heads, 64, dtype=torch.bfloat16)
+    if kind == "last_bits":
+        q[..., 1] = 2.0 ** -40
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    for k in (1, 2, 30, 299, 302, 500):
+        out, sel = cache.decode_sparse(q.to(DEV), i32([pages * 16]), k, sel=True)
+        check_attention(cfg, arrays, q, [pages * 16], out, top_k=k, sel=sel)
+
+
+@pytest.mark.parametrize("dtype,bits,d,group,batch", [("bf16", 4, 64, 1, 450), ("f32", 8, 256, 8, 1), ("bf16", 8, 128, 16, 300)])
+def test_sparse_with_the_longest_table(dtype, bits, d, group, batch):
+    """16384 pages a sequence and top_k = 512: the most shared memory a call asks for."""
+    r = np.random.default_rng(10)
+    lens = [int(x) for x in r.integers(0, 200, batch)]
+    lens[0] = 16384 * 16 if batch == 1 else 9000
+    cfg = config(batch=batch, kv_heads=1, q_heads=group, head_dim=d, page=16, max_pages=16384, n_pages=40, bits=bits, dtype=dtype)
+    arrays = fill(dict(cfg, batch=1, max_pages=1), 25)
+    arrays["table"] = r.integers(0, 40, (batch, 16384)).astype(np.int32)
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    q = queries(cfg)
+    out, sel = cache.decode_sparse(q.to(DEV), i32(lens), 512, sel=True)
+    check_attention(cfg, arrays, q, lens, out, top_k=512, sel=sel)
+
+
 def test_sparse_ties_and_nan_means():
     cfg = config(batch=1, kv_heads=1, q_heads=2, head_dim=64, page=16, max_pages=40)
     arrays = fill(cfg, 16)

@@ -81,7 +81,8 @@ def test_token_bytes():
 
 
 BAD = [dict(batch=0), dict(layers=0), dict(kv_heads=3), dict(q_heads=34), dict(page=24), dict(page=8), dict(page=512),
-       dict(max_pages=16385), dict(bits=3), dict(bits=16), dict(max_pages=0, n_pages=4), dict(batch=70000)]
+       dict(max_pages=16385), dict(bits=3), dict(bits=16), dict(max_pages=0, n_pages=4), dict(batch=70000),
+       dict(layers=64, kv_heads=8, n_pages=1 << 15, page=256)]   # 2^32 rows
 
 
 @pytest.mark.parametrize("kw", BAD)

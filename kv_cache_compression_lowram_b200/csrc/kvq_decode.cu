@@ -1,7 +1,9 @@
 // Quantised KV cache: attention of the last tokens over whole sequences.
 //
-// Bound by HBM: 2 (d bits / 8 + d / 16) bytes per cached token and KV head, read once per 8 or 16
-// query rows.  All steps of all units -- a unit is (sequence, layer, KV head, tile of query rows), a
+// Bound by HBM: 2 (d bits / 8 + d / 16) bytes per cached token and KV head, read once per 4, 8 or 16
+// query rows (4 layers of 4 x 32K tokens, 8 heads of 128 in 4 bits: 604 MB in 130 us, 4.6 TB/s, 71 % of the
+// measured copy rate; a further such layer costs 28.7 us, 5.3 TB/s) -- and, nearly as much, by the
+// instructions that unpack (48 % of the issue slots).  All steps of all units -- a unit is (sequence, layer, KV head, tile of query rows), a
 // step 16 or 32 of its tokens -- form one line that is shared out evenly among the CTAs (one wave of
 // them), so ragged lengths and few long sequences load the SMs alike without the host knowing a
 // length.
@@ -29,25 +31,15 @@ constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   //
 
 template <int BITS, int D, int ROWS, bool F32> struct Plan {
   using Tl = Tile<BITS, D, ROWS, F32>;
-  #ifdef KVQ_TB
-  static constexpr int TB = KVQ_TB;
-#else
-  static constexpr int TB = Tl::BLOCK <= 2304 ? 2 : 1;
-#endif      // 16-token blocks of a step
+  static constexpr int TB = Tl::BLOCK <= 2304 ? 2 : 1;      // 16-token blocks of a step: 32 tokens up to 4.6 KB
   static constexpr int SLOT = TB * Tl::BLOCK;
-  #ifdef KVQ_STAGES
-  static constexpr int STAGES = KVQ_STAGES;
-#else
   static constexpr int STAGES = SLOT > 4608 ? 2 : 3;
-#endif
   static constexpr int JOIN = kWarps * Tl::ROWS * D * 4;    // the warps' sums
   static constexpr int RING = kWarps * STAGES * SLOT;
   static constexpr int SMEM = RING + JOIN + Tl::QFRAG + Tl::QMETA + kWarps * Tl::ROWS * 8 + 16;
-  #ifdef KVQ_MINB
-  static constexpr int MINB = KVQ_MINB;
-#else
+  // Three CTAs an SM where the shared memory allows it (d = 128 in 4 bits, four rows: 12 warps of 168
+  // registers; two CTAs of 255 took 21 % longer, four of 128 11 %, and steps of 16 tokens 17 %).
   static constexpr int MINB = SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);
-#endif
 };
 
 struct Walk {   // a place on the line of steps

@@ -2,10 +2,11 @@
 //
 // Both are one pass over the caller's rows, bound by HBM: per K or V row of d channels,
 // d * sizeof(dt) bytes on one side and d * bits / 8 + d / 16 on the other (8 x 8192 tokens, 8 heads of 128,
-// bf16 and 4 bits, 344 MB: written in 94 us, 3.7 TB/s, read back in 66 us, 5.2 TB/s).  A CTA takes the
+// bf16 and 4 bits, 344 MB: written in 89 us, 3.9 TB/s, read back in 66 us, 5.2 TB/s).  A CTA takes the
 // part of one page that a call touches, for one (layer, sequence, KV head): the page's codes
 // and scales are one contiguous block each, the caller's rows are d-long pieces that
-// neighbouring CTAs (the next head) continue.  Half of its warps take K, half V.
+// neighbouring CTAs (the next head) continue.  Half of its warps take K, half V (writing has one
+// each: with two each, what a warp does once was a third of its instructions).
 //
 // Writing is limited by instructions as much as by memory, so numbers go two to a register (channels
 // k and k + 4 of a cell) through the packed fp32 operations, a lane holds 16 channels (4 lanes a
@@ -20,6 +21,7 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kWriteThreads = 64;   // a warp for K and one for V
 constexpr int kUnroll = 4;   // rows that a lane of the reading kernel has in flight
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -271,14 +273,11 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
 struct Piece {
   int layer, b, h, page, s0, s1, tok0;   // token of slot t: tok0 + t
 };
-__device__ __forceinline__ bool piece_of(const Args& a, const int32_t* pos, const int32_t* count, int pieces, Piece* p) {
-  unsigned x = blockIdx.x;
-  p->h = x % a.Hkv;
-  x /= a.Hkv;
-  const int j = x % pieces;
-  x /= pieces;
-  p->b = x % a.B;
-  p->layer = x / a.B;
+__device__ __forceinline__ bool piece_of(const Args& a, const int32_t* pos, const int32_t* count, Piece* p) {
+  const int j = blockIdx.x / a.Hkv;        // grid: (piece, head), sequence, layer
+  p->h = blockIdx.x - j * a.Hkv;
+  p->b = blockIdx.y;
+  p->layer = blockIdx.z;
   const long long p0 = __ldg(pos + p->b);
   int n = a.n;
   bool bad = false;
@@ -301,16 +300,16 @@ __device__ __forceinline__ bool piece_of(const Args& a, const int32_t* pos, cons
 }
 
 template <typename T, int BITS, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 6) write_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
-                                                         const int32_t* __restrict__ count, int pieces) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 2 * RPW, G = D / kGroup, ROW = D * BITS / 8, FLY = 2;
+__global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 14 : 12) write_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
+                                                         const int32_t* __restrict__ count) {
+  constexpr int LPR = D / 16, STEP = 32 / LPR, G = D / kGroup, ROW = D * BITS / 8, FLY = 2;
   __shared__ float sums[STEP][D];
   Piece p;
-  if (!piece_of(a, pos, count, pieces, &p)) return;
+  if (!piece_of(a, pos, count, &p)) return;
   const int pid = p.page < 0 ? -1 : page_of(a, p.b, p.page);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool is_v = warp >= 2;
-  const int rsub = (warp & 1) * RPW + lane / LPR, l16 = lane % LPR, grp = l16 / 4, cell = l16 % 4 * G + grp;
+  const bool is_v = warp == 1;
+  const int rsub = lane / LPR, l16 = lane % LPR, grp = l16 / 4, cell = l16 % 4 * G + grp;
   const int ch = grp * 64 + l16 % 4 * 8;   // the lane's channels: 8 from here on, and 8 that lie 32 further (every access whole sectors)
   const Rows& src = is_v ? v : k;
   const char* in = static_cast<const char*>(src.p) +
@@ -402,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 6) write_kernel
   __syncthreads();
   __nv_bfloat16* out = a.k_mean + (row0 >> a.page_log2) * D;
   const float inv = 1.f / (float)a.page;   // a power of two
-  for (int c = threadIdx.x; c < D; c += kThreads) {
+  for (int c = threadIdx.x; c < D; c += kWriteThreads) {
     float s = 0.f;
 #pragma unroll
     for (int r = 0; r < STEP; ++r) s += sums[r][c];
@@ -412,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 6) write_kernel
 
 template <typename T, int BITS, int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(Args a, Rows k, Rows v, const int32_t* __restrict__ pos,
-                                                        const int32_t* __restrict__ count, int pieces) {
+                                                        const int32_t* __restrict__ count) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 2 * RPW, G = D / kGroup, ROW = D * BITS / 8;
   Piece p;
-  if (!piece_of(a, pos, count, pieces, &p)) return;
+  if (!piece_of(a, pos, count, &p)) return;
   const int pid = p.page < 0 ? -1 : page_of(a, p.b, p.page);
   if (pid < 0 && p.page >= 0 && threadIdx.x == 0) flag(a, KVQ_ERR_PAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -455,10 +454,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Args a, Rows k, Rows v, 
 template <bool WRITE, typename T, int BITS>
 cudaError_t go(const Args& a, const Rows& k, const Rows& v, const int32_t* pos, const int32_t* count, cudaStream_t s) {
   const int pieces = ((a.n - 1) >> a.page_log2) + 2;   // a run of n tokens touches at most this many pages
-  const unsigned grid = (unsigned)((long long)pieces * a.n_layers * a.B * a.Hkv);
+  const dim3 grid((unsigned)pieces * a.Hkv, a.B, a.n_layers);
 #define LOWRAM_KVQ_GO(D)                                                              \
-  if constexpr (WRITE) write_kernel<T, BITS, D><<<grid, kThreads, 0, s>>>(a, k, v, pos, count, pieces); \
-  else read_kernel<T, BITS, D><<<grid, kThreads, 0, s>>>(a, k, v, pos, count, pieces)
+  if constexpr (WRITE) write_kernel<T, BITS, D><<<grid, kWriteThreads, 0, s>>>(a, k, v, pos, count); \
+  else read_kernel<T, BITS, D><<<grid, kThreads, 0, s>>>(a, k, v, pos, count)
   switch (a.d) {
     case 64: LOWRAM_KVQ_GO(64); break;
     case 128: LOWRAM_KVQ_GO(128); break;

@@ -576,7 +576,7 @@ uint64_t lowram_kvq_token_bytes(const lowram_kvq_config* cfg);
  *             written (NULL: all).
  * A page whose last slot is written gets its mean from all its tokens, earlier ones included:
  * write a sequence in order, from its end on (tokens dropped from the end may be written anew).
- * Two sequences of a call may not write into the same page. */
+ * A call may write a page through one place of one sequence only. */
 lowram_status lowram_kvq_write(const lowram_kvq_config* cfg, const lowram_kvq_cache* cache, int32_t layer0,
                                int32_t n_layers, int32_t n_new, const void* k, const int64_t* k_stride,
                                const void* v, const int64_t* v_stride, const int32_t* pos, const int32_t* count,

@@ -550,8 +550,11 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   }
 
   // ---------------------------------------------------------------- end
-  // Running maximum of column (t, c) in log2 units, -inf without a token.
-  __device__ __forceinline__ float top(int t, int c) const { return thr[t][c] == -INFINITY ? -INFINITY : -mneg[t][c]; }
+  // Running maximum of column (t, c) in log2 units, -inf without a token; after reduce().  (Where all
+  // scores were NaN no maximum was found, but the sum of the weights is NaN, and has to count.)
+  __device__ __forceinline__ float top(int t, int c) const {
+    return thr[t][c] == -INFINITY && l[t][c] == l[t][c] ? -INFINITY : -mneg[t][c];
+  }
   // Adds up what lanes hold apart: sums of the weights and of the offsets' part.
   __device__ __forceinline__ void reduce() {
 #pragma unroll

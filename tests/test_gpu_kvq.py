@@ -338,6 +338,32 @@ def test_nan_in_a_token_that_an_earlier_query_does_not_see(bits):
         arrays["k_scale"][0, p, 0, 39 % 16] = arrays["v_scale"][0, p, 0, 39 % 16] = np.float16(np.nan)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_and_infinite_queries_spoil_their_own_rows(bits, dtype):
+    """Also where every token's score is NaN, and in a sequence whose keys all are."""
+    cfg = config(batch=2, kv_heads=2, q_heads=8, page=16, max_pages=40, bits=bits, dtype=dtype)
+    arrays = fill(cfg, 26)
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    q = queries(cfg)
+    lens = [600, 35]
+    q[0, 0, 0, 1, 5], q[0, 0, 0, 6, 7], q[0, 1, 0, 3, 0] = float("nan"), float("inf"), float("-inf")
+    clean = torch.ones(2, 8, dtype=torch.bool)
+    clean[0, 1] = clean[0, 6] = clean[1, 3] = False
+    ref = q.clone()
+    ref[0, :, 0][~clean] = 0
+    got = cache.decode(q.to(DEV), i32(lens))
+    assert torch.isnan(got[0, :, 0].cpu()[~clean]).all()
+    got[0, :, 0][~clean.to(DEV)] = cache.decode(ref.to(DEV), i32(lens))[0, :, 0][~clean.to(DEV)]
+    check_attention(cfg, arrays, ref, lens, got)
+    out = cache.decode_sparse(q.to(DEV), i32(lens), 3)
+    assert torch.isnan(out[0, :, 0].cpu()[~clean]).all() and torch.isfinite(out[0, :, 0].cpu()[clean]).all()
+    arrays["k_scale"][:, arrays["table"][1]] = np.nan
+    bad = K.LowramKvq(cfg, to_device(arrays))
+    for out in (bad.decode(ref.to(DEV), i32(lens)), bad.decode_sparse(ref.to(DEV), i32(lens), 3)):
+        assert torch.isnan(out[0, 1]).all() and torch.isfinite(out[0, 0]).all()
+
+
 def test_refusals_on_the_device():
     cfg = config(batch=2, kv_heads=2, q_heads=4)
     cache = K.LowramKvq(cfg, to_device(fill(cfg, 23)))
@@ -530,6 +556,36 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(outs[r % 2], want)), r
         pos += 1
     assert cache.validate() == 0
+
+
+def test_first_calls_may_be_captured():
+    """A process whose first calls of the quantised cache are captured, and replayed on new data."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, kv_cache_compression_lowram_b200 as K
+c = K.LowramKvq(dict(batch=2, n_layers=1, n_kv_heads=2, n_q_heads=8, head_dim=128, page=16, n_pages=16, max_pages=8, bits=4, dtype="bf16"))
+x = torch.randn(1, 2, 100, 2, 128, device="cuda").bfloat16()
+q = torch.randn(1, 2, 1, 8, 128, device="cuda").bfloat16()
+pos, lens = (torch.full((2,), n, dtype=torch.int32, device="cuda") for n in (0, 100))
+out = [torch.zeros_like(x), torch.zeros_like(x)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c.write(x, x, pos)
+    c.read(pos, out=out)
+    a, b = c.decode(q, lens), c.decode_sparse(q, lens, 7)
+x.normal_()
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(a, c.decode(q, lens)) and torch.equal(b, c.decode_sparse(q, lens, 7)) and c.validate() == 0
+assert (out[0] - x).abs().max() < 0.5 and torch.equal(*out) and a.abs().max() > 0 and (a - b).abs().max() < 0.02
+print("captured")
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stderr[-2000:]
 
 
 @pytest.mark.parametrize("bits", [4, 8])

@@ -395,7 +395,9 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
       cluster.sync();
       float most_n = 0.f;
       for (int k = lane; k < CS * kWarps; k += 32) most_n = fmaxf(most_n, cluster.map_shared_rank(s.bound, k / kWarps)[k % kWarps]);
-      const float off = 9.5367432e-7f * sqrtf(qn) * sqrtf(warp_max(most_n));   // 2^-20
+      most_n = warp_max(most_n);
+      // 2^-20 of the norms; no bound where a square or a product may have underflowed
+      const float off = qn > 1e-25f && most_n > 1e-25f ? 9.5367432e-7f * sqrtf(qn) * sqrtf(most_n) : INFINITY;
       int mn = INT_MAX, mx = INT_MIN;
 #pragma unroll 8
       for (int c = tid; c < last; c += kThreads) {

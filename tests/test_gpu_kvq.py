@@ -389,7 +389,7 @@ def test_refusals_on_the_device():
     assert few.validate() == 0
 
 
-@pytest.mark.parametrize("kind", ["equal", "two_values", "last_bits"])
+@pytest.mark.parametrize("kind", ["equal", "two_values", "last_bits", "tiny_means", "tiny_queries", "large_means"])
 @pytest.mark.parametrize("heads", [1, 40])
 def test_sparse_scores_too_near_for_fp32(kind, heads):
     """More pages near the border than are ranked by comparison: equal means, two values, and means whose
@@ -406,7 +406,9 @@ def test_sparse_scores_too_near_for_fp32(kind, heads):
         m[0, r.permutation(pages)[:300], :, 0] = 1.5
     if kind == "last_bits":      # a channel whose product is 2^-40 of the score
         m[..., 1] = r.integers(0, 200, (1, pages, 1))
-    q = torch.ones(1, 1, 1, heads, 64, dtype=torch.bfloat16)
+    if kind in ("tiny_means", "tiny_queries", "large_means"):      # squares and products that leave fp32's range
+        m[:] = torch.tensor(r.standard_normal(m.shape) * {"tiny_means": 1e-22, "tiny_queries": 1e-3, "large_means": 1e22}[kind]).bfloat16().double().numpy()
+    q = torch.ones(1, 1, 1, heads, 64, dtype=torch.bfloat16) * (1e-37 if kind == "tiny_queries" else 1.0)
     if kind == "last_bits":
         q[..., 1] = 2.0 ** -40
     cache = K.LowramKvq(cfg, to_device(arrays))

@@ -6,23 +6,24 @@
 // rows waste little of a tile.  A code needs no conversion: its bits, masked in place in a
 // 16-bit lane, ARE an fp16 number -- code n in the low mantissa bits is the subnormal n 2^-24, four
 // bits higher n 2^-20 -- and products with subnormals are exact.  Unpacking is one mask per two
-// codes and one shift per four; a 4-bit cache streams from HBM at the rate at which the warps
-// unpack it (about 1.6 thread instructions a code at d = 128), which is why the matrix
-// instruction that takes A from registers is used: tcgen05 reads A from shared memory, where
-// every code would first have to be stored as 16 bits.
+// codes and one shift per four.  The tile is bound by its instructions (about 2.3 of a thread per code
+// at d = 128 in 4 bits, all of them counted) and their latencies, close to the rate at which HBM
+// delivers 4-bit codes; the tensor pipe is 22 % busy.  That is why the matrix instruction that takes
+// A from registers is used: tcgen05 reads A from shared memory, where every code would first have
+// to be stored as 16 bits.
 //
 // Scores.  x_t = sum_g s_tg (n_tg . q_g) + lo_tg sum(q_g): the scale and the offset of a group enter
-// per accumulator, in fp32, so keys are never rounded.  (fp32 calls
-// unpack to centred codes, and lose nothing to sums that cancel either.)  q is multiplied by a power of two per
-// row so that its largest entry lies in [2^13, 2^14): bf16 values stay exact in fp16 down to
-// 2^-27 of the largest (an fp32 q is split into two fp16 parts).
+// per accumulator, in fp32, so keys are never rounded.  (fp32 calls unpack to centred codes, and
+// lose nothing to sums that cancel either.)  q is multiplied by a power of two per row so that its
+// largest entry lies in [2^13, 2^14): bf16 values stay exact in fp16 down to 2^-27 of the largest
+// (an fp32 q is split into two fp16 parts).
 //
-// Values.  o_c = sum_t (p_t s_tg) (n_tc - mid) + sum_t p_t (lo_tg + mid s_tg): w = p s 2^-E (times a constant) is rounded to fp16 once (fp32
-// calls: split in two parts), E following the value scales so that w stays within fp16's
-// normal range; the offsets are summed in fp32 beside.  A step's products are summed on their own
-// and added to the output in fp32 (the tensor core's sums are cut off, not rounded).  p = 2^(x - m) with a running m that moves
-// only when a score passes it by some factor -- w then still fits -- so most tiles neither reduce a
-// maximum across lanes nor rescale.
+// Values.  o_c = sum_t (p_t s_tg) (n_tc - mid) + sum_t p_t (lo_tg + mid s_tg): w = p s 2^-E (times a
+// constant) is rounded to fp16 once (fp32 calls: split in two parts), E following the value scales so
+// that w stays within fp16's normal range; the offsets are summed in fp32 beside.  A step's products
+// are summed on their own and added to the output in fp32 (the tensor core's sums are cut off, not
+// rounded).  p = 2^(x - m) with a running m that moves only when a score passes it by some factor --
+// w then still fits -- so most tiles neither reduce a maximum across lanes nor rescale.
 //
 // Lane l holds r = l / 4, q = l % 4:
 //   A of the scores:  tokens r, r + 8; the cells 2q, 2q + 1 of every group -- one contiguous piece

@@ -560,6 +560,34 @@ def test_streams_and_graphs():
     assert cache.validate() == 0
 
 
+def test_two_streams_at_once():
+    """Two caches over the same arrays, each with its workspace, attend and read at the same time on the
+    streams that their calls are given."""
+    cfg = config(batch=4, layers=2, kv_heads=4, q_heads=16, page=32, max_pages=130)
+    arrays = fill(dict(cfg, n_pages=200, batch=1, max_pages=1), 27)
+    cfg["n_pages"] = 200
+    arrays["table"] = np.random.default_rng(12).integers(0, 200, (4, 130)).astype(np.int32)
+    dev = to_device(arrays)
+    lens = i32([4100, 77, 3000, 1])
+    q = queries(cfg, 2).to(DEV)
+    one = K.LowramKvq(cfg, dev, max_q=2)
+    want = one.decode(q, lens), one.decode_sparse(q, lens, 9), one.read(i32([0, 7, 64, 0]), n=64)[0]
+    caches, streams = [one, K.LowramKvq(cfg, dev, max_q=2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    rounds = 8
+    outs = [[(torch.empty_like(q), torch.empty_like(q), torch.empty_like(want[2]), torch.empty_like(want[2])) for _ in range(rounds)] for _ in caches]
+    pos = i32([0, 7, 64, 0])
+    torch.cuda.synchronize()
+    for r in range(rounds):
+        for c, s, o in zip(caches, streams, outs):
+            c.decode(q, lens, out=o[r][0], stream=s)
+            c.decode_sparse(q, lens, 9, out=o[r][1], stream=s)
+            c.read(pos, out=o[r][2:], stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        for r in o:
+            assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1]) and torch.equal(r[2], want[2])
+
+
 def test_first_calls_may_be_captured():
     """A process whose first calls of the quantised cache are captured, and replayed on new data."""
     import os

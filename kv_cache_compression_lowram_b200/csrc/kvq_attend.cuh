@@ -150,9 +150,12 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   static constexpr bool QREG = STEPS * NT * SPQ * 2 <= 16;       // B operands kept in registers
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   // A score may pass the running maximum by a factor of 2^kSlack in its weight, a value scale leave
-  // [2^E, 2^(E+1)) by a factor of kWide either way: w <= 2^(kSlack + 1) kWide kBias < 2^16, and what
-  // fp16's smallest step (2^-24) loses is 2^-30 (fp32: 2^-34) of a weight of one.
-  static constexpr float kSlack = F32 ? 2.f : 4.f, kWide = F32 ? 8.f : 16.f, kBias = F32 ? 1024.f : 64.f;
+  // [2^E, 2^(E+1)) by a factor of kWide either way: w <= 2^(kSlack + 1) kWide kBias = 2^15, half of what
+  // fp16 holds (the other factor of two is for roundings), and what fp16's smallest step (2^-24) loses
+  // is 2^-30 (fp32: 2^-33) of a weight of one.
+  static constexpr int kSlackLog2 = F32 ? 2 : 4;
+  static constexpr float kSlack = kSlackLog2, kWide = F32 ? 8.f : 16.f, kBias = F32 ? 512.f : 64.f;
+  static_assert((1 << kSlackLog2) * 2.f * kWide * kBias <= 32768.f, "weights must stay within fp16");
 
   // What a code is multiplied by to be a number: fp32 calls centre their codes and have the 1.
   static constexpr float kCode = F32 ? 1.f : 16777216.f;

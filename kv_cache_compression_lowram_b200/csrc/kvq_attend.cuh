@@ -22,7 +22,7 @@
 // constant) is rounded to fp16 once (fp32 calls: split in two parts), E following the value scales so
 // that w stays within fp16's normal range; the offsets are summed in fp32 beside.  A step's products
 // are summed on their own and added to the output in fp32 (the tensor core's sums are cut off, not
-// rounded).  p = 2^(x - m) with a running m that moves only when a score passes it by some factor --
+// rounded).  p = 2^(f (x - m)) with a running m that moves only when a score passes it by some factor --
 // w then still fits -- so most tiles neither reduce a maximum across lanes nor rescale.
 //
 // Lane l holds r = l / 4, q = l % 4:
@@ -167,7 +167,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 
   // [..][i * CP + c]: A's row r + 8 i, the lane's c-th column
   float o[NT][G][4][2 * CP], ls[NT][G][CP], l[NT][CP], qs[NT][G][CP];
-  float f[NT][CP], mneg[NT][CP], thr[NT][CP];
+  float f[NT][CP], mx[NT][CP], thr[NT][CP];           // f'', the running maximum (0 before the first), when it moves
   float unit_inv;                                     // kBias 2^-E, 0 before the first scale
   uint32_t top_s;                                     // the largest scale that needs no new unit (fp16 bits)
   uint2 qr[QREG ? STEPS * NT * SPQ : 1];
@@ -253,7 +253,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
       for (int c = 0; c < CP; ++c) {
         const int j = row_of(t, c);
         f[t][c] = meta[j];
-        mneg[t][c] = 0.f;
+        mx[t][c] = 0.f;
         thr[t][c] = -INFINITY;
         l[t][c] = 0.f;
 #pragma unroll
@@ -406,7 +406,8 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < 2 * CP; ++k) {
-          const float p = ex2(fmaf(x[b][t][k], f[t][k % CP], mneg[t][k % CP]));
+          // the difference first: a product rounded to fp32 is off by much more than one for scores above 2^25
+          const float p = ex2((x[b][t][k] - mx[t][k % CP]) * f[t][k % CP]);
           x[b][t][k] = p;
           l[t][k % CP] += p;
         }
@@ -527,17 +528,16 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < CP; ++c) {
-        float mx = -INFINITY;
+        float most = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < TB; ++b) mx = fmaxf(mx, fmaxf(x[b][t][c], x[b][t][CP + c]));
+        for (int b = 0; b < TB; ++b) most = fmaxf(most, fmaxf(x[b][t][c], x[b][t][CP + c]));
 #pragma unroll
-        for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, i));
+        for (int i = 4; i < 32; i <<= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, i));
         float alpha = 1.f;
-        if (mx > thr[t][c]) {
-          const float m = -mx * f[t][c];
-          alpha = thr[t][c] == -INFINITY ? 0.f : ex2(m - mneg[t][c]);
-          mneg[t][c] = m;
-          thr[t][c] = mx + kSlack / f[t][c];
+        if (most > thr[t][c]) {
+          alpha = thr[t][c] == -INFINITY ? 0.f : ex2((mx[t][c] - most) * f[t][c]);
+          mx[t][c] = most;
+          thr[t][c] = __fadd_rd(most, kSlack / f[t][c]);   // rounded down: no weight above 2^kSlack
           l[t][c] *= alpha;
         }
         const float both = alpha * scale;
@@ -554,11 +554,14 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   }
 
   // ---------------------------------------------------------------- end
-  // Running maximum of column (t, c) in log2 units, -inf without a token; after reduce().  (Where all
-  // scores were NaN no maximum was found, but the sum of the weights is NaN, and has to count.)
+  // Running maximum of column (t, c), -inf without a token; after reduce().  (Where all scores were
+  // NaN no maximum was found, but the sum of the weights is NaN, and has to count.)
   __device__ __forceinline__ float top(int t, int c) const {
-    return thr[t][c] == -INFINITY && l[t][c] == l[t][c] ? -INFINITY : -mneg[t][c];
+    return thr[t][c] == -INFINITY && l[t][c] == l[t][c] ? -INFINITY : mx[t][c];
   }
+  // What sums with the running maximum m are multiplied by to be joined under the maximum `to`; f: the
+  // row's f''.
+  static __device__ __forceinline__ float factor(float m, float to, float f) { return m == -INFINITY ? 0.f : ex2((m - to) * f); }
   // Adds up what lanes hold apart: sums of the weights and of the offsets' part.
   __device__ __forceinline__ void reduce() {
 #pragma unroll

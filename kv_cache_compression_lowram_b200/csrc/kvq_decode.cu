@@ -36,7 +36,7 @@ template <int BITS, int D, int ROWS, bool F32> struct Plan {
   static constexpr int STAGES = SLOT > 4608 ? 2 : 3;
   static constexpr int JOIN = kWarps * Tl::ROWS * D * 4;    // the warps' sums
   static constexpr int RING = kWarps * STAGES * SLOT;
-  static constexpr int SMEM = RING + JOIN + Tl::QFRAG + Tl::QMETA + kWarps * Tl::ROWS * 8 + 16;
+  static constexpr int SMEM = RING + JOIN + Tl::QFRAG + Tl::QMETA + (kWarps + 1) * Tl::ROWS * 8 + 16;
   // Three CTAs an SM where the shared memory allows it (d = 128 in 4 bits, four rows: 12 warps of 168
   // registers; two CTAs of 255 took 21 % longer, four of 128 11 %, and steps of 16 tokens 17 %).
   static constexpr int MINB = SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);
@@ -105,9 +105,9 @@ template <class P> struct Line {
 
 // The parts of a unit (CTAs c_first .. c_last), joined in their order.  A warp per row finds the
 // weights of a chunk of parts, then each thread sums four channels over them with its loads in
-// flight together.  wt: [kChunk][ROWS] floats; norm: [ROWS] maxima, then [ROWS] sums.
+// flight together.  wt: [kChunk][ROWS] floats; f: the rows' f''; norm: [ROWS] maxima, then [ROWS] sums.
 template <class P, class Store>
-__device__ __forceinline__ void join_parts(const float* part, int c_first, int c_last, int rows, float* wt, float* norm, Store store) {
+__device__ __forceinline__ void join_parts(const float* part, int c_first, int c_last, int rows, float* wt, const float* f, float* norm, Store store) {
   constexpr int ROWS = P::Tl::ROWS, D = P::Tl::D, REC = ROWS * (D + 2), kChunk = P::JOIN / 4 / ROWS, FLY = 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = c_last - c_first + 1;
   auto at = [&](int i) { return part + (size_t)(2 * (c_first + i) + (i == 0 ? 1 : 0)) * REC; };
@@ -139,7 +139,7 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
       for (int i = lane, k = 0; i < nc; i += 32, ++k) {
         const float* p = at(i0 + i) + ROWS * D + j;
         const float mi = k == 0 ? mp[0] : (k == 1 ? mp[1] : __ldcg(p)), li = k == 0 ? lp[0] : (k == 1 ? lp[1] : __ldcg(p + ROWS));
-        const float w = mi == -INFINITY ? 0.f : ex2(mi - m);
+        const float w = P::Tl::factor(mi, m, f[j]);
         wt[i * ROWS + j] = w;
         l += w == 0.f ? 0.f : w * li;
       }
@@ -188,7 +188,8 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
   float* join = reinterpret_cast<float*>(frag + Tl::QFRAG);
   float* meta = join + P::JOIN / 4;
   float* tops = meta + Tl::QMETA / 4;          // [warp][row] running maxima, then the sums of the weights
-  int* shared_int = reinterpret_cast<int*>(tops + 2 * kWarps * ROWS);
+  float* norm = tops + 2 * kWarps * ROWS;      // [ROWS] maxima, [ROWS] sums of the CTA
+  int* shared_int = reinterpret_cast<int*>(norm + 2 * ROWS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const T* q = static_cast<const T*>(qv);
   T* out = static_cast<T*>(outv);
@@ -407,19 +408,18 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
       return m;
     };
     tile.store_out(join + warp * ROWS * D, [&](int j) {
-      const float mine = tops[warp * ROWS + j];
-      return mine == -INFINITY ? 0.f : ex2(mine - most(j));
+      return Tl::factor(tops[warp * ROWS + j], most(j), meta[j]);
     });
-    if (tid < ROWS) {                           // meta has done its work
+    if (tid < ROWS) {
       const float m = most(tid);
       float l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = tops[w * ROWS + tid];
-        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], ex2(mw - m), l);
+        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], Tl::factor(mw, m, meta[tid]), l);
       }
-      meta[tid] = m;
-      meta[ROWS + tid] = l;
+      norm[tid] = m;
+      norm[ROWS + tid] = l;
     }
     __syncthreads();
     const bool whole = cur.st == 0 && part_n == cur.n;
@@ -444,11 +444,11 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
         const float4 y = *reinterpret_cast<const float4*>(join + (w * ROWS + j) * D + c);
         v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
       }
-      if (whole) finish(j, c, v, meta[j], meta[ROWS + j]);
+      if (whole) finish(j, c, v, norm[j], norm[ROWS + j]);
       else *reinterpret_cast<float4*>(rec + 4 * e) = v;
     }
     if (!whole) {
-      if (tid < 2 * ROWS) rec[ROWS * D + tid] = meta[tid];
+      if (tid < 2 * ROWS) rec[ROWS * D + tid] = norm[tid];
       // the last CTA of the unit to come joins all parts, in their order
       int c0 = c_first, c1 = c_last;
       if (c0 < 0) {
@@ -465,7 +465,7 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
         *shared_int = last;
       }
       __syncthreads();
-      if (*shared_int) join_parts<P>(part, c0, c1, rows, join, meta, finish);
+      if (*shared_int) join_parts<P>(part, c0, c1, rows, join, meta, norm, finish);
     }
     __syncthreads();                            // the queries' operands and the sums may be written anew
     x += part_n;

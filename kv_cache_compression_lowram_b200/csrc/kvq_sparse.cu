@@ -549,8 +549,7 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
       return m;
     };
     tile.store_out(join + warp * ROWS * D, [&](int j) {
-      const float top = tops[warp * ROWS + j];
-      return top == -INFINITY ? 0.f : ex2(top - most(j));
+      return Tl::factor(tops[warp * ROWS + j], most(j), meta[j]);
     });
     if (tid < ROWS) {
       const float m = most(tid);
@@ -558,7 +557,7 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = tops[w * ROWS + tid];
-        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], ex2(mw - m), l);
+        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], Tl::factor(mw, m, meta[tid]), l);
       }
       norm[tid] = m;
       norm[ROWS + tid] = l;
@@ -586,7 +585,7 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
       float4 v = reinterpret_cast<const float4*>(cluster.map_shared_rank(join, src))[in ? e : 0];
       float l = nr[ROWS + j], m = mr;
       for (int o = 1; o < CS; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      const float w = mr == -INFINITY ? 0.f : ex2(mr - m);
+      const float w = Tl::factor(mr, m, meta[j]);
       l = w == 0.f ? 0.f : l * w;
       v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
       for (int o = 1; o < CS; o <<= 1) {

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import kv_cache_compression_lowram_b200 as K
-from kvq_utils import DT, check_attention, config, fill, queries, to_device
+from kvq_utils import DT, U16, UBF, check_attention, config, fill, queries, to_device
+from oracle import kvq as O
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -41,3 +42,40 @@ def test_weights_at_the_top_of_their_range(bits, dtype, d, group, sparse):
     out = cache.decode_sparse(q.to(DEV), i32([n]), n // 64) if sparse else cache.decode(q.to(DEV), i32([n]))
     assert torch.isfinite(out).all()
     check_attention(cfg, arrays, q, [n], out)
+
+
+def check_one_token(bits, dtype, d, group, q_log2, k_log2):
+    """Scores so far apart that the softmax is one token's value: |o - v| is at most the rounding of the
+    weight (fp16 in BF16 calls) and of the output."""
+    lens = [700, 90]
+    cfg = config(batch=2, kv_heads=1, q_heads=group, head_dim=d, page=16, max_pages=44, bits=bits, dtype=dtype)
+    arrays = fill(cfg, 31, k_std=2.0 ** k_log2)
+    q = queries(cfg, std=2.0 ** q_log2)
+    assert torch.isfinite(q).all()
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    outs = [cache.decode(q.to(DEV), i32(lens))] + [cache.decode_sparse(q.to(DEV), i32(lens), 44)]
+    checked = 0
+    for b in range(2):
+        k, v = (O.rows(arrays[x + "_code"][0, arrays["table"][b], 0], arrays[x + "_scale"][0, arrays["table"][b], 0], bits).reshape(-1, d)[:lens[b]]
+                for x in "kv")
+        x = q[0, b, 0].double().numpy() @ k.T / d ** 0.5
+        for j in range(group):
+            best, second = np.sort(x[j])[[-1, -2]]
+            # scores are sums in fp32 (d + 12 roundings): the best is the best, and the rest is nothing
+            if best - second < 80 + 4 * (d + 12) * 2.0 ** -24 * np.abs(q[0, b, 0, j].double().numpy()) @ np.abs(k).max(0) / d ** 0.5:
+                continue
+            checked += 1
+            ref, M = v[x[j].argmax()], np.abs(v[x[j].argmax()]).max() + 16
+            for out in outs:
+                got = out[0, b, 0, j].double().cpu().numpy()
+                tol = 2.0 ** -20 * M + (U16 * M + UBF * np.abs(ref) if dtype == "bf16" else 0.0)
+                assert (np.abs(got - ref) <= tol).all(), (b, j, got[:4], ref[:4])
+    assert checked >= group
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 4), (128, 16), (256, 8)])
+@pytest.mark.parametrize("q_log2,k_log2", [(12, 10), (15, 10), (17, 11), (20, 12), (30, 12), (100, 0), (112, -4)])
+def test_large_scores_choose_one_token(bits, dtype, d, group, q_log2, k_log2):
+    check_one_token(bits, dtype, d, group, q_log2, k_log2)

@@ -554,10 +554,10 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   }
 
   // ---------------------------------------------------------------- end
-  // Running maximum of column (t, c), -inf without a token; after reduce().  (Where all scores were
-  // NaN no maximum was found, but the sum of the weights is NaN, and has to count.)
+  // Running maximum of column (t, c), -inf without a token; after reduce().  Where a score was NaN the
+  // sum of the weights is, and counts against any other maximum: as +inf, whose factor is NaN.
   __device__ __forceinline__ float top(int t, int c) const {
-    return thr[t][c] == -INFINITY && l[t][c] == l[t][c] ? -INFINITY : mx[t][c];
+    return l[t][c] != l[t][c] ? INFINITY : (thr[t][c] == -INFINITY ? -INFINITY : mx[t][c]);
   }
   // What sums with the running maximum m are multiplied by to be joined under the maximum `to`; f: the
   // row's f''.
@@ -587,7 +587,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         }
     }
   }
-  // The unnormalised outputs [ROWS][D], times weight(row) (0: left out; its sums may be anything).
+  // The unnormalised outputs [ROWS][D], times weight(row) (0 leaves NaN of the values as it is).
   template <class Weight> __device__ __forceinline__ void store_out(float* to, Weight weight) const {
     const int r = (threadIdx.x & 31) >> 2;
     const float u0 = unit_inv == 0.f ? 0.f : kCode / unit_inv, u1 = BITS == 4 ? u0 * 0.0625f : u0;
@@ -602,7 +602,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 v = make_float2(fmaf(o[t][g][k][c], u0, ls[t][g][c]), fmaf(o[t][g][k][CP + c], u1, ls[t][g][c]));
-            *reinterpret_cast<float2*>(to + j * D + 64 * g + 8 * r + 2 * k) = w == 0.f ? make_float2(0.f, 0.f) : make_float2(v.x * w, v.y * w);
+            *reinterpret_cast<float2*>(to + j * D + 64 * g + 8 * r + 2 * k) = make_float2(v.x * w, v.y * w);
           }
       }
   }

@@ -141,7 +141,7 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
         const float mi = k == 0 ? mp[0] : (k == 1 ? mp[1] : __ldcg(p)), li = k == 0 ? lp[0] : (k == 1 ? lp[1] : __ldcg(p + ROWS));
         const float w = P::Tl::factor(mi, m, f[j]);
         wt[i * ROWS + j] = w;
-        l += w == 0.f ? 0.f : w * li;
+        l = fmaf(w, li, l);
       }
       l = warp_sum(l);
       if (lane == 0) norm[ROWS + j] = i0 ? norm[ROWS + j] + l : l;
@@ -158,12 +158,10 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
 #pragma unroll
         for (int f = 0; f < FLY; ++f) {
           const float w = i + f < nc ? wt[(i + f) * ROWS + j] : 0.f;
-          if (w != 0.f) {
-            v[k].x = fmaf(w, x[f].x, v[k].x);
-            v[k].y = fmaf(w, x[f].y, v[k].y);
-            v[k].z = fmaf(w, x[f].z, v[k].z);
-            v[k].w = fmaf(w, x[f].w, v[k].w);
-          }
+          v[k].x = fmaf(w, x[f].x, v[k].x);
+          v[k].y = fmaf(w, x[f].y, v[k].y);
+          v[k].z = fmaf(w, x[f].z, v[k].z);
+          v[k].w = fmaf(w, x[f].w, v[k].w);
         }
       }
     }
@@ -416,7 +414,7 @@ decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t*
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = tops[w * ROWS + tid];
-        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], Tl::factor(mw, m, meta[tid]), l);
+        l = fmaf(tops[(kWarps + w) * ROWS + tid], Tl::factor(mw, m, meta[tid]), l);
       }
       norm[tid] = m;
       norm[ROWS + tid] = l;

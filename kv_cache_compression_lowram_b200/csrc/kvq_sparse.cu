@@ -557,7 +557,7 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = tops[w * ROWS + tid];
-        if (mw != -INFINITY) l = fmaf(tops[(kWarps + w) * ROWS + tid], Tl::factor(mw, m, meta[tid]), l);
+        l = fmaf(tops[(kWarps + w) * ROWS + tid], Tl::factor(mw, m, meta[tid]), l);
       }
       norm[tid] = m;
       norm[ROWS + tid] = l;
@@ -586,8 +586,8 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
       float l = nr[ROWS + j], m = mr;
       for (int o = 1; o < CS; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
       const float w = Tl::factor(mr, m, meta[j]);
-      l = w == 0.f ? 0.f : l * w;
-      v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+      l *= w;
+      v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
       for (int o = 1; o < CS; o <<= 1) {
         l += __shfl_xor_sync(kFull, l, o);
         v.x += __shfl_xor_sync(kFull, v.x, o);

@@ -79,3 +79,24 @@ def check_one_token(bits, dtype, d, group, q_log2, k_log2):
 @pytest.mark.parametrize("q_log2,k_log2", [(12, 10), (15, 10), (17, 11), (20, 12), (30, 12), (100, 0), (112, -4)])
 def test_large_scores_choose_one_token(bits, dtype, d, group, q_log2, k_log2):
     check_one_token(bits, dtype, d, group, q_log2, k_log2)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 4), (128, 16), (256, 8)])
+def test_nan_spoils_its_row_however_large_the_other_scores(bits, dtype, d, group):
+    """A token of NaN among scores that lie thousands apart: the part of the sequence that holds it has no
+    weight against the others, and the row (for a key) or the group (for a value) is NaN all the same."""
+    lens = [700, 300]
+    cfg = config(batch=2, kv_heads=1, q_heads=group, head_dim=d, page=16, max_pages=44, bits=bits, dtype=dtype)
+    arrays = fill(cfg, 34)
+    q = queries(cfg, std=2.0 ** 12)
+    k = O.rows(arrays["k_code"][0, arrays["table"][0], 0], arrays["k_scale"][0, arrays["table"][0], 0], bits).reshape(-1, d)[:700]
+    low = int((q[0, 0, 0].double().numpy() @ k.T).max(0).argmin())
+    for x, spoilt in (("k", d), ("v", 64)):
+        bad = dict(arrays, **{x + "_scale": arrays[x + "_scale"].copy()})
+        bad[x + "_scale"][0, arrays["table"][0, low // 16], 0, low % 16, 0, 1] = np.nan
+        cache = K.LowramKvq(cfg, to_device(bad))
+        for out in (cache.decode(q.to(DEV), i32(lens)), cache.decode_sparse(q.to(DEV), i32(lens), 44)):
+            assert torch.isnan(out[0, 0, ..., :spoilt]).all() and torch.isfinite(out[0, 0, ..., spoilt:]).all()
+            assert torch.isfinite(out[0, 1]).all()

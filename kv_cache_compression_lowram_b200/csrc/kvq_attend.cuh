@@ -215,16 +215,19 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         for (int i = 0; i < PER; ++i) {
           x[i] = to_f<T>(raw[k][i]);
           mx = fmaxf(mx, fabsf(x[i]));
-          sum += x[i];
         }
         mx = warp_max(mx);
         // a power of two: 2^13 <= mx sigma < 2^14 (1 for a row of zeros, or with an infinity)
         const int e = (int)(__float_as_uint(mx) >> 23) - 127;
         const float sigma = e > -127 && e < 128 ? __uint_as_float((unsigned)(min(13 - e, 100) + 127) << 23) : 1.f;
 #pragma unroll
+        for (int i = 0; i < PER; ++i) sum = fmaf(x[i], sigma, sum);   // scaled first: a sum of entries may pass fp32's range
+#pragma unroll
         for (int i = 16 / G; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);   // 32 / G lanes hold a group
-        if (lane == 0) meta[j] = kLog2e * rsqrtf((float)D) * (kCode / sigma);
-        if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * sigma * (1.f / kCode);
+        // At most 2^100 (queries from 2^113 on): scores that differ, by 2^-72 or more with what fp16 holds of q,
+        // are millions apart in log2 units there, and a smaller factor gives the same weights, 0 and 1.
+        if (lane == 0) meta[j] = fminf(kLog2e * rsqrtf((float)D) * (kCode / sigma), 1.2676506e30f);
+        if (lane % (32 / G) == 0) meta[ROWS + j * G + lane / (32 / G)] = sum * (1.f / kCode);
         const int col = CP == 1 ? 2 * j : j % 8, tile = CP == 1 ? 0 : j / 8;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {

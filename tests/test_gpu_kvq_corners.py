@@ -84,6 +84,14 @@ def test_large_scores_choose_one_token(bits, dtype, d, group, q_log2, k_log2):
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d,group", [(64, 2), (128, 4), (128, 16), (256, 8)])
+@pytest.mark.parametrize("q_log2,k_log2", [(118, -10), (122, -12), (126, -14)])
+def test_queries_near_the_largest_number(bits, dtype, d, group, q_log2, k_log2):
+    check_one_token(bits, dtype, d, group, q_log2, k_log2)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 4), (128, 16), (256, 8)])
 def test_nan_spoils_its_row_however_large_the_other_scores(bits, dtype, d, group):
     """A token of NaN among scores that lie thousands apart: the part of the sequence that holds it has no
     weight against the others, and the row (for a key) or the group (for a value) is NaN all the same."""

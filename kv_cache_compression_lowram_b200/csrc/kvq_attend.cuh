@@ -19,7 +19,7 @@
 // (an fp32 q is split into two fp16 parts).
 //
 // Values.  o_c = sum_t (p_t s_tg) (n_tc - mid) + sum_t p_t (lo_tg + mid s_tg): w = p s 2^-E (times a
-// constant) is rounded to fp16 once (fp32 calls: split in two parts), E following the value scales so
+// constant) is rounded to fp16 once (fp32 calls: split in two parts), E following a group's value scales so
 // that w stays within fp16's normal range; the offsets are summed in fp32 beside.  A step's products
 // are summed on their own and added to the output in fp32 (the tensor core's sums are cut off, not
 // rounded).  p = 2^(f (x - m)) with a running m that moves only when a score passes it by some factor --
@@ -168,8 +168,8 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // [..][i * CP + c]: A's row r + 8 i, the lane's c-th column
   float o[NT][G][4][2 * CP], ls[NT][G][CP], l[NT][CP], qs[NT][G][CP];
   float f[NT][CP], mx[NT][CP], thr[NT][CP];           // f'', the running maximum (0 before the first), when it moves
-  float unit_inv;                                     // kBias 2^-E, 0 before the first scale
-  uint32_t top_s;                                     // the largest scale that needs no new unit (fp16 bits)
+  float unit_inv[G];                                  // of a group of channels: kBias 2^-E, 0 before the first scale
+  uint32_t top_s[(G + 1) / 2];                        // the largest scales that need no new unit (fp16 bits, two groups each)
   uint2 qr[QREG ? STEPS * NT * SPQ : 1];
 
   // The query row of this lane's column (t, c).
@@ -267,8 +267,11 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
           for (int k = 0; k < 4; ++k) o[t][g][k][c] = o[t][g][k][CP + c] = 0.f;
         }
       }
-    unit_inv = 0.f;
-    top_s = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      unit_inv[g] = 0.f;
+      top_s[g / 2] = 0;
+    }
   }
   __device__ __forceinline__ uint2 qop(const uint8_t* frag, int i) const {
     if constexpr (QREG) return qr[i];
@@ -373,7 +376,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
       }
     }
     // value scales and offsets of the tokens r, r + 8
-    uint32_t vm[N][2][G], most_s = 0;   // (s, lo) pairs; the largest s in the low half (s >= 0, so its bits are ordered)
+    uint32_t vm[N][2][G], most_s[G];    // (s, lo) pairs; a group's largest s in the low half (s >= 0, so its bits are ordered)
 #pragma unroll
     for (int b = 0; b < N; ++b)
 #pragma unroll
@@ -389,12 +392,18 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
             for (int g = 0; g < G; ++g) vm[b][i][g] = 0;
         }
-        if constexpr (G == 1) most_s = __vmaxu2(most_s, vm[b][i][0]);
-        else
-#pragma unroll
-          for (int g = 0; g < G; g += 2) most_s = __vimax3_u16x2(most_s, vm[b][i][g], vm[b][i][g + 1]);
       }
-    bool high = (most_s & 0xffffu) > top_s;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      most_s[g] = __vmaxu2(vm[0][0][g], vm[0][1][g]);
+      if constexpr (N == 2) most_s[g] = __vimax3_u16x2(most_s[g], vm[N - 1][0][g], vm[N - 1][1][g]);
+    }
+    bool high = false;
+#pragma unroll
+    for (int g = 0; g < G; g += 2) {
+      const uint32_t two = G > 1 ? __byte_perm(most_s[g], most_s[G > 1 ? g + 1 : g], 0x5410) : most_s[g] & 0xffffu;
+      high |= __vmaxu2(two, top_s[g / 2]) != top_s[g / 2];
+    }
 #pragma unroll
     for (int b = 0; b < N; ++b)
 #pragma unroll
@@ -438,7 +447,7 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
 #pragma unroll
           for (int e = 0; e < (CP == 1 && G > 1 ? 2 : 1); ++e) {
             const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&vm[b][i][CP == 2 ? gs : 2 * gs + e]));
-            u[i][e] = make_float2(m.x * unit_inv, fmaf(kMid, m.x, m.y));
+            u[i][e] = make_float2(m.x * unit_inv[CP == 2 ? gs : 2 * gs + e], fmaf(kMid, m.x, m.y));
           }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -508,24 +517,32 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // has become far too large is made smaller here as well: the scales it was made for have lost
   // their weight only if the maximum has moved.
   template <int TB> __device__ __forceinline__ void move(const float (&x)[TB][NT][2 * CP], const uint32_t (&vm)[TB][2][G]) {
-    uint32_t sb = 0;   // the largest finite scale (one that is not spoils the rows that see it, but not the unit)
+    float scale[G];
+    uint32_t sb[G];   // the largest finite scale (one that is not spoils the rows that see it, but not the unit)
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+    for (int g = 0; g < G; ++g) {
+      sb[g] = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int b = 0; b < TB; ++b)
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+        for (int i = 0; i < 2; ++i) {
           const uint32_t s16 = vm[b][i][g] & 0xffffu;
-          sb = max(sb, s16 < 0x7c00u ? s16 : 0u);
+          sb[g] = max(sb[g], s16 < 0x7c00u ? s16 : 0u);
         }
-    sb = __reduce_max_sync(kFull, sb);
-    const float s = __half2float(__ushort_as_half((unsigned short)sb));
-    float scale = 1.f;
-    if (sb && (unit_inv == 0.f || sb > top_s || !(s * unit_inv > kBias / kWide))) {
-      const float inv = kBias * __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);   // kBias <= s inv < 2 kBias
-      scale = unit_inv == 0.f ? 1.f : inv / unit_inv;
-      unit_inv = inv;
-      top_s = __half_as_ushort(__float2half_rz(fminf(kWide * 2.f * kBias / inv, 65504.f)));   // a power of two
+      sb[g] = __reduce_max_sync(kFull, sb[g]);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t top = g & 1 ? top_s[g / 2] >> 16 : top_s[g / 2] & 0xffffu;
+      const float s = __half2float(__ushort_as_half((unsigned short)sb[g])), old = unit_inv[g];
+      const bool anew = sb[g] && (old == 0.f || sb[g] > top || !(s * old > kBias / kWide));
+      // powers of two, whose reciprocals are exponents: kBias <= s inv < 2 kBias
+      const uint32_t two_e = __float_as_uint(s) & 0x7f800000u;
+      const float inv = kBias * __uint_as_float((254u << 23) - two_e), over = old == 0.f ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(old));
+      const uint32_t room = __half_as_ushort(__float2half_rz(fminf(kWide * 2.f * __uint_as_float(two_e), 65504.f)));
+      scale[g] = anew && old != 0.f ? inv * over : 1.f;
+      unit_inv[g] = anew ? inv : old;
+      if (anew) top_s[g / 2] = __byte_perm(top_s[g / 2], room, g & 1 ? 0x5410 : 0x3254);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -540,12 +557,12 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         if (most > thr[t][c]) {
           alpha = thr[t][c] == -INFINITY ? 0.f : ex2((mx[t][c] - most) * f[t][c]);
           mx[t][c] = most;
-          thr[t][c] = __fadd_rd(most, kSlack / f[t][c]);   // rounded down: no weight above 2^kSlack
+          thr[t][c] = __fadd_rd(most, __fdividef(kSlack, f[t][c]));   // rounded down: no weight above 2^kSlack
           l[t][c] *= alpha;
         }
-        const float both = alpha * scale;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
+          const float both = alpha * scale[g];
           ls[t][g][c] *= alpha;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -593,7 +610,6 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
   // The unnormalised outputs [ROWS][D], times weight(row) (0 leaves NaN of the values as it is).
   template <class Weight> __device__ __forceinline__ void store_out(float* to, Weight weight) const {
     const int r = (threadIdx.x & 31) >> 2;
-    const float u0 = unit_inv == 0.f ? 0.f : kCode / unit_inv, u1 = BITS == 4 ? u0 * 0.0625f : u0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -601,12 +617,14 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         const int j = row_of(t, c);
         const float w = weight(j);
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int g = 0; g < G; ++g) {
+          const float u0 = unit_inv[g] == 0.f ? 0.f : kCode * __uint_as_float((254u << 23) - __float_as_uint(unit_inv[g])), u1 = BITS == 4 ? u0 * 0.0625f : u0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 v = make_float2(fmaf(o[t][g][k][c], u0, ls[t][g][c]), fmaf(o[t][g][k][CP + c], u1, ls[t][g][c]));
             *reinterpret_cast<float2*>(to + j * D + 64 * g + 8 * r + 2 * k) = make_float2(v.x * w, v.y * w);
           }
+        }
       }
   }
 };

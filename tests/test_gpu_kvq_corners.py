@@ -108,3 +108,28 @@ def test_nan_spoils_its_row_however_large_the_other_scores(bits, dtype, d, group
         for out in (cache.decode(q.to(DEV), i32(lens)), cache.decode_sparse(q.to(DEV), i32(lens), 44)):
             assert torch.isnan(out[0, 0, ..., :spoilt]).all() and torch.isfinite(out[0, 0, ..., spoilt:]).all()
             assert torch.isfinite(out[0, 1]).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,group", [(128, 3), (128, 8), (128, 16), (256, 4), (256, 8)])
+@pytest.mark.parametrize("small_first", [False, True])
+def test_groups_of_unlike_scale(bits, dtype, d, group, small_first):
+    """Value groups 2^28 apart: every channel is as near to its own group's values as if it were alone."""
+    lens = [300, 41]
+    cfg = config(batch=2, kv_heads=1, q_heads=group, head_dim=d, page=16, max_pages=20, bits=bits, dtype=dtype)
+    arrays = fill(cfg, 32)
+    G = d // 64
+    std = np.array([2.0 ** (13 if (g % 2 == 0) != small_first else -15) for g in range(G)])
+    v = np.random.default_rng(33).standard_normal((1, cfg["n_pages"], 1, 16, d)) * np.repeat(std, 64)
+    n, s = O.quantise(v, bits)
+    arrays["v_code"], arrays["v_scale"] = O.pack(n, bits), s
+    q = queries(cfg)
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    for out in (cache.decode(q.to(DEV), i32(lens)), cache.decode_sparse(q.to(DEV), i32(lens), 20)):
+        for g in range(G):      # one group at a time, the others' values taken out of the bound
+            one = dict(arrays, v_scale=arrays["v_scale"].copy())
+            one["v_scale"][..., [x for x in range(G) if x != g], :] = 0
+            got = out.clone()
+            got.view(*got.shape[:-1], G, 64)[..., [x for x in range(G) if x != g], :] = 0
+            check_attention(cfg, one, q, lens, got)

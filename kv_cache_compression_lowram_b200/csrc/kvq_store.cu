@@ -211,7 +211,7 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
       const float2 e = fma2(nf[k], minus_s, t).get();
       near = max_abs(near, e.x, e.y);
     }
-    if (near >= hs) {
+    if (near >= hs && g.usable) {   // (a group without a scale has codes of 0)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 e = fma2(nf[k], minus_s, add2(raw.pair(k), minus_lo)).get();

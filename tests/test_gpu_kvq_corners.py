@@ -133,3 +133,73 @@ def test_groups_of_unlike_scale(bits, dtype, d, group, small_first):
             got = out.clone()
             got.view(*got.shape[:-1], G, 64)[..., [x for x in range(G) if x != g], :] = 0
             check_attention(cfg, one, q, lens, got)
+
+
+# ------------------------------------------------------------------------ writing
+
+def written_rows(x, bits, d, dtype):
+    """(codes, scales, read back) of rows x [n][d] after a write as keys and values."""
+    n = x.shape[0]
+    page = 256
+    cfg = config(batch=1, kv_heads=1, q_heads=1, head_dim=d, page=page, max_pages=-(-n // page), bits=bits, dtype=dtype)
+    cache = K.LowramKvq(cfg)
+    t = x.to(DT[dtype]).view(1, 1, n, 1, d).to(DEV)
+    cache.write(t, t, i32([0]))
+    back = cache.read(i32([0]), n=n)
+    assert torch.equal(cache.arrays["k_code"], cache.arrays["v_code"]) and torch.equal(back[0].view(torch.uint8), back[1].view(torch.uint8))
+    code, scale = (cache.arrays[k].cpu().numpy()[0, :-(-n // page), 0] for k in ("k_code", "k_scale"))
+    return code.reshape(-1, code.shape[-1])[:n], scale.reshape(-1, d // 64, 2)[:n], back[0][0, 0, :, 0].cpu()
+
+
+def check_rows(x, bits, d, dtype):
+    x = x.to(DT[dtype])
+    code, scale, back = written_rows(x, bits, d, dtype)
+    n, s = O.quantise(x.double().numpy(), bits)
+    bad = np.argwhere(scale.view(np.uint16) != s.view(np.uint16))
+    assert not len(bad), (len(bad), bad[:4].tolist())
+    bad = np.argwhere(O.unpack(code, bits) != n)
+    assert not len(bad), (len(bad), bad[:4].tolist())
+    assert torch.equal(back, torch.tensor(O.dequantise(n, s)).float().to(DT[dtype]))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_groups_without_a_scale(bits, dtype, d):
+    """Constant groups and ranges below fp16's smallest scale: s = 0 and every code 0."""
+    x = torch.zeros(40, d)
+    for i, c in enumerate((1e-8, -1e-8, 1e-6, 1.5e-7, 3.3e-5, 1.2345678, -777.7, 6e4, 2.0 ** -24, 2.0 ** -25, 1e-41)):
+        x[i] = c
+    g = torch.Generator().manual_seed(1)
+    x[20:30] = 1e-8 * torch.randn(10, d, generator=g)
+    x[30:40] = 2.0 ** -24 * (1 + torch.rand(10, d, generator=g)) * ((1 << bits) - 1) / 8
+    check_rows(x, bits, d, dtype)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_write_odd_values_bf16(bits):
+    """Small ranges beside large values, tiny and large values, codes and half steps exactly; a group with
+    NaN or infinity reads back non-finite and disturbs no other."""
+    d, n, q = 128, 64, (1 << bits) - 1
+    x = torch.randn(n, d, generator=torch.Generator().manual_seed(1)).double()
+    x[2] = 1000 + 8 * x[2].round()
+    x[3] = -1000 + 4 * x[3]
+    x[4] *= 1e-7
+    x[5] *= 1e-5
+    x[6] *= 1e4
+    x[7] = torch.arange(d) % (q + 1) * 0.5
+    x[8] = (torch.arange(d) % q + 0.5) * 0.25
+    x[8, ::64], x[8, 1::64] = 0.0, q * 0.25
+    x[9] = x[9].abs() * 1e-38
+    x[10] = -6e4
+    x[10, 5::64] = 6e4
+    check_rows(x, bits, d, "bf16")
+    x[20, 3], x[21, 70], x[22, 9], x[23, 65] = float("nan"), float("inf"), -float("inf"), 3e38
+    got = written_rows(x, bits, d, "bf16")[2]
+    clean = torch.ones(n, d, dtype=torch.bool)
+    for r, c in ((20, 0), (21, 64), (22, 0), (23, 64)):
+        clean[r, c:c + 64] = False
+        assert not torch.isfinite(got[r, c:c + 64]).all()
+    x[~clean] = 0
+    codes, scale = O.quantise(x.bfloat16().double().numpy(), bits)
+    assert torch.equal(got[clean], torch.tensor(O.dequantise(codes, scale)).float().bfloat16()[clean])

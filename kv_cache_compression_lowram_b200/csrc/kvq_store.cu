@@ -40,6 +40,12 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// min(|a|, |b|, |c|)
+__device__ __forceinline__ float min_abs(float a, float b, float c) {
+  float r;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -198,46 +204,7 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
   const F2 magic(kMagic), unmagic(-kMagic), inv(g.inv);
   float near = 0.f;
   bool exact = !g.inside;
-  if constexpr (sizeof(T) == 2) {
-    // t = x - lo is exact (but for x below 2^-16 of lo), and so is the remainder e = t - n s: a code
-    // is right where |e| < s / 2.  Values of 8 bits do meet half steps: every 28th group of 64 normal
-    // values has one in 4 bits.
-    const float hs = 0.5f * g.s;
-    const F2 minus_lo(-g.lo), minus_s(-g.s);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const F2 t = add2(raw.pair(k), minus_lo);
-      nf[k] = add2(fma2(t, inv, magic), unmagic);
-      const float2 e = fma2(nf[k], minus_s, t).get();
-      near = max_abs(near, e.x, e.y);
-    }
-    if (near >= hs && g.usable) {   // (a group without a scale has codes of 0)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 e = fma2(nf[k], minus_s, add2(raw.pair(k), minus_lo)).get();
-        float2 n = nf[k].get();
-        auto odd = [](float x) { return __float_as_uint(x + kMagic) & 1u; };
-        if (fabsf(e.x) > hs || (fabsf(e.x) == hs && odd(n.x))) n.x += copysignf(1.f, e.x);
-        if (fabsf(e.y) > hs || (fabsf(e.y) == hs && odd(n.y))) n.y += copysignf(1.f, e.y);
-        nf[k] = F2(n.x, n.y);
-      }
-    }
-  } else {
-    // f = x inv + off = (x - lo) / s up to (2 kQ + |off|) 2^-24 (inv, off and the sum are each off by
-    // 2^-24 relative), rounded by adding kMagic.  A value nearer than twice that to a half step takes
-    // the exact path below.
-    const float tie = 0.5f - (2.f * kQ + fabsf(g.off)) * 1.1920929e-7f;
-    const F2 off(g.off), minus(-1.f);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const F2 f = fma2(raw.pair(k), inv, off);
-      nf[k] = add2(add2(f, magic), unmagic);
-      const float2 e = fma2(nf[k], minus, f).get();
-      near = max_abs(near, e.x, e.y);
-    }
-    exact |= !(near < tie);
-  }
-  if (exact && g.usable) {
+  auto exactly = [&]() {   // all codes anew
     auto code = [&](float x) {
       // t + te = x - lo exactly; n the nearest code up to one; m = t - n s exactly (n s has 19 bits and
       // is within s of t); so the sign of 2 (m + te) -+ s is known
@@ -255,7 +222,51 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
       const float2 x = raw.pair(k).get();
       nf[k] = F2(code(x.x), code(x.y));
     }
+  };
+  if constexpr (sizeof(T) == 2) {
+    // t = x - lo is exact but for x below 2^-16 of lo, and so is the remainder e = t - n s: a code is
+    // right where |e| < s / 2.  (Half steps are fp32 numbers, so a t that was rounded lies on the same
+    // side of them as x - lo, or meets one: then the codes are made exactly.)  Values of 8 bits do meet
+    // half steps: every 28th group of 64 normal values has one in 4 bits.
+    const float hs = 0.5f * g.s;
+    const F2 minus_lo(-g.lo), minus_s(-g.s);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const F2 t = add2(raw.pair(k), minus_lo);
+      nf[k] = add2(fma2(t, inv, magic), unmagic);
+      const float2 e = fma2(nf[k], minus_s, t).get();
+      near = max_abs(near, e.x, e.y);
+    }
+    if (near >= hs && g.usable) {   // (a group without a scale has codes of 0)
+      float least = INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = raw.pair(k).get(), e = fma2(nf[k], minus_s, add2(raw.pair(k), minus_lo)).get();
+        least = min_abs(least, x.x, x.y);
+        float2 n = nf[k].get();
+        auto odd = [](float x) { return __float_as_uint(x + kMagic) & 1u; };
+        if (fabsf(e.x) > hs || (fabsf(e.x) == hs && odd(n.x))) n.x += copysignf(1.f, e.x);
+        if (fabsf(e.y) > hs || (fabsf(e.y) == hs && odd(n.y))) n.y += copysignf(1.f, e.y);
+        nf[k] = F2(n.x, n.y);
+      }
+      if (least < 3.0517578e-5f * fabsf(g.lo)) exactly();   // 2^-15
+    }
+  } else {
+    // f = x inv + off = (x - lo) / s up to (2 kQ + |off|) 2^-24 (inv, off and the sum are each off by
+    // 2^-24 relative), rounded by adding kMagic.  A value nearer than twice that to a half step takes
+    // the exact path below.
+    const float tie = 0.5f - (2.f * kQ + fabsf(g.off)) * 1.1920929e-7f;
+    const F2 off(g.off), minus(-1.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const F2 f = fma2(raw.pair(k), inv, off);
+      nf[k] = add2(add2(f, magic), unmagic);
+      const float2 e = fma2(nf[k], minus, f).get();
+      near = max_abs(near, e.x, e.y);
+    }
+    exact |= !(near < tie);
   }
+  if (exact && g.usable) exactly();
   // four codes (two of 8 bits) in one fp32 number, whose integer then lies in its low mantissa bits
   const F2 bias(8388608.f);
   auto words = [&](F2 x) { const float2 y = add2(x, bias).get(); return make_uint2(__float_as_uint(y.x), __float_as_uint(y.y)); };

@@ -1,5 +1,7 @@
 """Corners of the quantised KV cache's value ranges on the GPU, against the fp64 oracle."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -174,6 +176,29 @@ def test_groups_without_a_scale(bits, dtype, d):
     x[20:30] = 1e-8 * torch.randn(10, d, generator=g)
     x[30:40] = 2.0 ** -24 * (1 + torch.rand(10, d, generator=g)) * ((1 << bits) - 1) / 8
     check_rows(x, bits, d, dtype)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_beside_a_half_step(bits, dtype):
+    """Offset and step put a half step at 0: tiny values on both sides of it, and 0 itself."""
+    d, q = 128, (1 << bits) - 1
+    tiny = [sign * 2.0 ** -e for e in (10, 17, 20, 24, 25, 30, 60, 100, 126, 133) for sign in (1, -1)] + [0.0]
+    rows = []
+    for step in (1.0, 0.25, 2.0 ** -9):
+        for first in range(0, len(tiny), 8):
+            r = torch.zeros(d)
+            r[0::64], r[1::64] = -q / 2 * step, q / 2 * step
+            for i, t in enumerate(tiny[first:first + 8]):
+                r[2 + 7 * i::64] = t
+            rows.append(r)
+    x = torch.stack(rows).to(DT[dtype])
+    code, scale, _ = written_rows(x, bits, d, dtype)
+    for r in range(len(rows)):      # in fractions: the smallest of these are below 2^-53 of the offset
+        s, lo = (Fraction(float(y)) for y in scale[r, 0])
+        assert (scale[r] == scale[r, 0]).all() and lo == -q * s / 2
+        want = [min(max(round((Fraction(float(y)) - lo) / s), 0), q) for y in x[r]]
+        assert O.unpack(code[r], bits).tolist() == want, r
 
 
 @pytest.mark.parametrize("bits", [4, 8])

@@ -167,6 +167,12 @@ __device__ __forceinline__ float2 group_range(const Raw8<__nv_bfloat16> (&raw)[2
   return make_float2(__low2float(m), -__high2float(m));
 }
 
+// What t = x - y, rounded to fp32, has lost: x - y = t + lost(x, y, t) exactly (two-sum).
+__device__ __forceinline__ float lost(float x, float y, float t) {
+  const float z = t - x;
+  return (x - (t - z)) + (-y - z);
+}
+
 // What the codes of a group are made with.
 struct Scale {
   float s, lo, inv, off;
@@ -178,10 +184,11 @@ __device__ __forceinline__ Scale scale_of(float2 range, __half2& meta) {
   const float mn = range.x, mx = range.y;
   float sf;
   if constexpr (sizeof(T) == 2) {
-    // (bf16 values differ exactly in fp32 unless one is below 2^-16 of the other.)  A correctly
-    // rounded quotient by the constant: one step of residual correction.
+    // The range (exact in fp32 unless one end is below 2^-16 of the other; what is lost joins the
+    // remainder) over the constant, correctly rounded: Markstein's correction of a quotient by its
+    // remainder ("IA-64 and Elementary Functions", 2000), with the constant's rounded reciprocal.
     const float span = mx - mn, q = span * kInvQ;
-    sf = fmaf(fmaf(-q, kQ, span), kInvQ, q);
+    sf = fmaf(fmaf(-q, kQ, span) + lost(mx, mn, span), kInvQ, q);
   } else {
     sf = (float)(((double)mx - (double)mn) / (double)kQ);
   }
@@ -208,7 +215,7 @@ __device__ __forceinline__ void codes_of(const Raw8<T>& raw, const Scale& g, Cel
     auto code = [&](float x) {
       // t + te = x - lo exactly; n the nearest code up to one; m = t - n s exactly (n s has 19 bits and
       // is within s of t); so the sign of 2 (m + te) -+ s is known
-      const float t = x - g.lo, z = t - x, te = (x - (t - z)) + (-g.lo - z);
+      const float t = x - g.lo, te = lost(x, g.lo, t);
       float n = fminf(fmaxf(t * g.inv, -1.f), kQ + 1.f);
       n = (n + kMagic) - kMagic;
       const float m = fmaf(-n, g.s, t), above = (2.f * m - g.s) + 2.f * te, below = (2.f * m + g.s) + 2.f * te;

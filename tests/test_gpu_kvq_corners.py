@@ -202,6 +202,26 @@ def test_values_beside_a_half_step(bits, dtype):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ranges_that_fp32_rounds(bits, dtype):
+    """One end of the range is so small beside the other that their distance has more than 24 bits: the
+    scale is still the format's, fp16 of fp32 of the exact quotient."""
+    d = 64
+    rows = [(1.8671875, -1.8477439880371094e-06), (1.6171875, -5.781650543212891e-06), (1.1171875, -1.341104507446289e-05),
+            (1.3671875, -9.47713851928711e-06)]
+    rows += [(-b, -a) for a, b in rows]
+    r = np.random.default_rng(4)
+    for _ in range(500):
+        a, b = (1 + r.integers(0, 128, 2) / 128) * 2.0 ** np.array([0, -r.integers(8, 40)])
+        rows.append((a, -b) if r.random() < 0.5 else (b, -a))
+    x = torch.zeros(len(rows), d, dtype=torch.float64)
+    for i, (hi, lo) in enumerate(rows):
+        x[i, 0::2], x[i, 1::2] = hi, lo
+    x = torch.cat([x * 2.0 ** e for e in (0, 14, -9)])
+    check_rows(x, bits, d, dtype)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 def test_write_odd_values_bf16(bits):
     """Small ranges beside large values, tiny and large values, codes and half steps exactly; a group with
     NaN or infinity reads back non-finite and disturbs no other."""

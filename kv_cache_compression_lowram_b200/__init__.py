@@ -893,6 +893,23 @@ class LowramKvq:
         if t.device != self.device:
             raise ValueError("the tensors of a call must be on the cache's device")
 
+    def _fresh(self, make, stream):
+        """The tensor of make(), for a call on ``stream``: taken from that stream's memory, so that no work
+        still under way elsewhere uses it, and not given back before the current stream is done with it."""
+        if stream is None:
+            return make()
+        torch, _, raw = _kvq_torch()
+        if _stream(stream) == raw(self.device.index):
+            return make()
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                      else torch.cuda.default_stream(self.device))
+        current = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            t = make()
+        t.record_stream(current)
+        return t
+
     def write(self, k, v, pos, count=None, layer0: int = 0, stream=None) -> None:
         """Quantise k, v [n_layers][B][n][Hkv][d] into slots pos[b] .. pos[b] + count[b] - 1."""
         self._mine(k)
@@ -914,10 +931,11 @@ class LowramKvq:
         return out
 
     def decode(self, q, lens, out=None, layer0: int = 0, stream=None):
-        """Attention of q [n_layers][B][n_q][Hq][d] over whole sequences of lens[b] tokens."""
+        """Attention of q [n_layers][B][n_q][Hq][d] over whole sequences of lens[b] tokens.  With ``stream``
+        and without ``out``, the result's memory belongs to ``stream``, as that of a torch operation there."""
         self._mine(q)
         if out is None:
-            out = _kvq_torch()[0].empty_like(q)
+            out = self._fresh(lambda: _kvq_torch()[0].empty_like(q), stream)
         lowram_kvq_decode_attn(self._calls, None, layer0, q, lens, out, self._workspace, stream)
         return out
 
@@ -926,9 +944,9 @@ class LowramKvq:
         self._mine(q)
         torch = _kvq_torch()[0]
         if out is None:
-            out = torch.empty_like(q)
-        s = torch.empty(tuple(q.shape[:3]) + (self.config.n_kv_heads, top_k), dtype=torch.int32,
-                        device=q.device) if sel else None
+            out = self._fresh(lambda: torch.empty_like(q), stream)
+        s = self._fresh(lambda: torch.empty(tuple(q.shape[:3]) + (self.config.n_kv_heads, top_k), dtype=torch.int32,
+                                            device=q.device), stream) if sel else None
         lowram_kvq_sparse_attn(self._calls, None, layer0, top_k, q, lens, out, s, stream)
         return (out, s) if sel else out
 

@@ -952,7 +952,8 @@ class LowramKvq:
 
     def validate(self) -> int:
         """The error word (bit 0: bad page id, bit 1: bad length, position or count), then cleared.
-        Synchronises."""
+        Waits for all work on the cache's device, whatever stream its calls were given."""
+        _kvq_torch()[0].cuda.synchronize(self.device)
         err = int(self.arrays["err"].item())
         if err:
             self.arrays["err"].zero_()

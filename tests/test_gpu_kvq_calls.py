@@ -49,3 +49,16 @@ def test_outputs_are_taken_on_the_stream_of_the_call(raw):
         got = cache.decode(q, lens, stream=stream)
     torch.cuda.synchronize()
     assert torch.equal(got, cache.decode(q, lens))
+
+
+def test_validate_waits_for_calls_on_other_streams():
+    cfg = config(batch=2, kv_heads=2, q_heads=4, page=16, max_pages=4)
+    cache = K.LowramKvq(cfg, to_device(fill(cfg, 41)))
+    q, out, lens = queries(cfg).to(DEV), queries(cfg).to(DEV), i32([65, 3])
+    side = torch.cuda.Stream()
+    for call in (lambda: cache.decode(q, lens, out=out, stream=side), lambda: cache.decode_sparse(q, lens, 2, out=out, stream=side)):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(LONG)
+        call()
+        assert cache.validate() == 2 and cache.validate() == 0

@@ -678,10 +678,10 @@ def _kvq_layouts(c) -> dict:
             "err": ((1,), torch.int32)}
 
 
-def _kvq_cache_struct(c, arrays) -> LowramKvqCacheC:
-    """Pointers of the caller's tensors, after a check of their types, shapes and device."""
+def _kvq_cache_struct(c, arrays):
+    """(pointers of the caller's tensors, their device), after a check of types, shapes and device."""
     if isinstance(arrays, LowramKvqCacheC):
-        return arrays
+        return arrays, None      # the caller answers for the device
     out = LowramKvqCacheC()
     dev = None
     for name, (shape, dtype) in _kvq_layouts(c).items():
@@ -699,7 +699,7 @@ def _kvq_cache_struct(c, arrays) -> LowramKvqCacheC:
         if t.dtype != dtype or tuple(t.shape) != shape:
             raise ValueError(f"{name} must be {dtype} of shape {shape}, not {t.dtype} of {tuple(t.shape)}")
         setattr(out, name, _ptr(t))
-    return out
+    return out, dev
 
 
 _KVQ = None
@@ -778,10 +778,19 @@ class _KvqPrepared:
 
     def __init__(self, c, arrays):
         torch = _kvq_torch()[0]
-        self.config, self.cache = c, _kvq_cache_struct(c, arrays)
+        self.config = c
+        self.cache, self.device = _kvq_cache_struct(c, arrays)
         self.c, self.k = ctypes.byref(self.config), ctypes.byref(self.cache)
         self.dims = (c.batch, c.n_kv_heads, c.n_q_heads, c.head_dim, torch.float32 if c.dtype == 0 else torch.bfloat16,
                      torch.int32, (c.batch,))
+
+
+def _kvq_device(p, t):
+    """The device of a call's tensor, which must be that of the cache's arrays."""
+    dev = t.device
+    if p.device is not None and dev != p.device:
+        raise ValueError("the tensors of a call must be on the device of the cache's arrays")
+    return dev
 
 
 def lowram_kvq_token_bytes(cfg) -> int:
@@ -801,7 +810,7 @@ def lowram_kvq_write(cfg, arrays, layer0: int, k, v, pos, count=None, stream=Non
     p = _kvq_prepared(cfg, arrays)
     kp, ks, layers, n = _kvq_rows(p.dims, k, "k")
     vp, vs, _, _ = _kvq_rows(p.dims, v, "v", layers, n)
-    dev = k.device
+    dev = _kvq_device(p, k)
     if v.device != dev:
         raise ValueError("k and v must be on one device")
     _kvq_call(lib().lowram_kvq_write, "lowram_kvq_write", dev, stream, p.c, p.k, layer0, layers, n, kp, ks, vp, vs,
@@ -813,7 +822,7 @@ def lowram_kvq_read(cfg, arrays, layer0: int, k_out, v_out, pos, count=None, str
     p = _kvq_prepared(cfg, arrays)
     kp, ks, layers, n = _kvq_rows(p.dims, k_out, "k_out")
     vp, vs, _, _ = _kvq_rows(p.dims, v_out, "v_out", layers, n)
-    dev = k_out.device
+    dev = _kvq_device(p, k_out)
     if v_out.device != dev:
         raise ValueError("k_out and v_out must be on one device")
     _kvq_call(lib().lowram_kvq_read, "lowram_kvq_read", dev, stream, p.c, p.k, layer0, layers, n, kp, ks, vp, vs,
@@ -842,7 +851,7 @@ def lowram_kvq_decode_attn(cfg, arrays, layer0: int, q, lens, out, workspace, st
     sequences of lens[b] tokens.  ``workspace``: lowram_kvq_workspace_bytes bytes, zeroed once."""
     p = _kvq_prepared(cfg, arrays)
     qp, op, layers, n = _kvq_queries(p.dims, q, out)
-    dev = q.device
+    dev = _kvq_device(p, q)
     if workspace.device != dev:
         raise ValueError("workspace must be on the device of q")
     _kvq_call(lib().lowram_kvq_decode_attn, "lowram_kvq_decode_attn", dev, stream, p.c, p.k, layer0, layers, n, qp,
@@ -854,7 +863,7 @@ def lowram_kvq_sparse_attn(cfg, arrays, layer0: int, top_k: int, q, lens, out, s
     [n_layers][B][n_q][Hkv][top_k] int32 takes their places in the sequence (then -1)."""
     p = _kvq_prepared(cfg, arrays)
     qp, op, layers, n = _kvq_queries(p.dims, q, out)
-    dev = q.device
+    dev = _kvq_device(p, q)
     if sel is not None and (tuple(sel.shape) != (layers, p.dims[0], n, p.dims[1], top_k) or sel.dtype is not p.dims[5]
                             or sel.device != dev):
         raise ValueError("sel must be int32 [n_layers][batch][n_q][n_kv_heads][top_k] on the device of q")
@@ -889,10 +898,6 @@ class LowramKvq:
         self._workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
         torch.cuda.current_stream(dev).synchronize()   # ready for whichever stream comes first
 
-    def _mine(self, t) -> None:
-        if t.device != self.device:
-            raise ValueError("the tensors of a call must be on the cache's device")
-
     def _fresh(self, make, stream):
         """The tensor of make(), for a call on ``stream``: taken from that stream's memory, so that no work
         still under way elsewhere uses it, and not given back before the current stream is done with it."""
@@ -912,7 +917,6 @@ class LowramKvq:
 
     def write(self, k, v, pos, count=None, layer0: int = 0, stream=None) -> None:
         """Quantise k, v [n_layers][B][n][Hkv][d] into slots pos[b] .. pos[b] + count[b] - 1."""
-        self._mine(k)
         lowram_kvq_write(self._calls, None, layer0, k, v, pos, count, stream)
 
     def read(self, pos, count=None, n: Optional[int] = None, layer0: int = 0, n_layers: Optional[int] = None, out=None,
@@ -926,14 +930,12 @@ class LowramKvq:
             c = self.config
             shape = (c.n_layers - layer0 if n_layers is None else n_layers, c.batch, n, c.n_kv_heads, c.head_dim)
             out = tuple(torch.zeros(shape, dtype=_kvq_dtype(c), device=self.device) for _ in range(2))
-        self._mine(out[0])
         lowram_kvq_read(self._calls, None, layer0, out[0], out[1], pos, count, stream)
         return out
 
     def decode(self, q, lens, out=None, layer0: int = 0, stream=None):
         """Attention of q [n_layers][B][n_q][Hq][d] over whole sequences of lens[b] tokens.  With ``stream``
         and without ``out``, the result's memory belongs to ``stream``, as that of a torch operation there."""
-        self._mine(q)
         if out is None:
             out = self._fresh(lambda: _kvq_torch()[0].empty_like(q), stream)
         lowram_kvq_decode_attn(self._calls, None, layer0, q, lens, out, self._workspace, stream)
@@ -941,7 +943,6 @@ class LowramKvq:
 
     def decode_sparse(self, q, lens, top_k: int, out=None, sel: bool = False, layer0: int = 0, stream=None):
         """The same over each query's newest page and its top_k - 1 best older pages."""
-        self._mine(q)
         torch = _kvq_torch()[0]
         if out is None:
             out = self._fresh(lambda: torch.empty_like(q), stream)

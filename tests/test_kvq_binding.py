@@ -1,0 +1,51 @@
+"""The Python side of the quantised KV cache without a GPU: tensors that only say they are on one."""
+
+import pytest
+import torch
+
+import kv_cache_compression_lowram_b200 as K
+from kvq_utils import config
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that calls itself one of a GPU."""
+
+    is_cuda = True
+    device = property(lambda self: torch.device("cuda", self.index))
+
+
+def on_gpu(index, *shape, dtype=torch.bfloat16):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+    t.index = index
+    return t
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    """What reaches the library is a failure."""
+    def reached(*_):
+        raise AssertionError("the call reached the library")
+    monkeypatch.setattr(K, "_kvq_call", reached)
+
+
+CFG = config(batch=2, layers=1, kv_heads=2, q_heads=4, page=16, max_pages=2)
+
+
+def arrays(index):
+    return {n: on_gpu(index, *shape, dtype=dtype) for n, (shape, dtype) in K._kvq_layouts(K.kvq_config_struct(CFG)).items()}
+
+
+def calls(a, index):
+    x, q = on_gpu(index, 1, 2, 3, 2, 128), on_gpu(index, 1, 2, 1, 4, 128)
+    pos, ws = on_gpu(index, 2, dtype=torch.int32), on_gpu(index, 64, dtype=torch.uint8)
+    return [lambda: K.lowram_kvq_write(CFG, a, 0, x, x, pos), lambda: K.lowram_kvq_read(CFG, a, 0, x, x, pos),
+            lambda: K.lowram_kvq_decode_attn(CFG, a, 0, q, pos, q, ws), lambda: K.lowram_kvq_sparse_attn(CFG, a, 0, 2, q, pos, q)]
+
+
+def test_data_on_another_device_than_the_arrays_is_refused(no_library):
+    for call in calls(arrays(0), 1):
+        with pytest.raises(ValueError, match="device"):
+            call()
+    for call in calls(arrays(1), 1):      # the same calls with everything on one device go on
+        with pytest.raises(AssertionError, match="reached"):
+            call()

@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import types
 from typing import Optional
 
 __all__ = [
@@ -163,7 +164,7 @@ def _check(status: int, where: str) -> None:
 # --------------------------------------------------------------------------- marshalling
 
 def _get(cfg, name):
-    return cfg[name] if isinstance(cfg, dict) else getattr(cfg, name)
+    return cfg[name] if isinstance(cfg, (dict, types.MappingProxyType)) else getattr(cfg, name)
 
 
 def config_struct(cfg) -> LowramConfigC:
@@ -877,7 +878,9 @@ class LowramKvq:
 
     ``cfg``: the fields of ``lowram_kvq_config``; ``arrays``: k_code, k_scale, v_code, v_scale and
     optionally k_mean and table (layouts of ``lowram.h``).  Without ``arrays`` they are allocated
-    on ``device``, with ``table`` as given (or none: sequence b owns pages b * max_pages + i)."""
+    on ``device``, with ``table`` as given (or none: sequence b owns pages b * max_pages + i).
+    ``LowramKvq.arrays`` shows the tensors in use; write into them (a new table, say), a cache on other
+    tensors is another ``LowramKvq``."""
 
     def __init__(self, cfg, arrays=None, max_q: int = 1, table=None, device="cuda"):
         import torch
@@ -888,13 +891,15 @@ class LowramKvq:
             arrays = {n: torch.zeros(shape, dtype=dtype, device=device)
                       for n, (shape, dtype) in _kvq_layouts(c).items() if n not in ("table", "err")}
             arrays["table"] = table
-        get = lambda n: arrays.get(n) if isinstance(arrays, dict) else getattr(arrays, n, None)  # noqa: E731
-        self.arrays = {n: get(n) for n in _kvq_layouts(c)}
-        self._calls = _KvqPrepared(c, self.arrays)
-        self.device = dev = self.arrays["k_code"].device
-        if self.arrays["err"] is None:
-            self.arrays["err"] = torch.zeros(1, dtype=torch.int32, device=dev)
-            self._calls.cache.err = self.arrays["err"].data_ptr()
+        def get(n):
+            return arrays.get(n) if isinstance(arrays, (dict, types.MappingProxyType)) else getattr(arrays, n, None)
+        held = {n: get(n) for n in _kvq_layouts(c)}
+        self._calls = _KvqPrepared(c, held)
+        self.device = dev = held["k_code"].device
+        if held["err"] is None:
+            held["err"] = torch.zeros(1, dtype=torch.int32, device=dev)
+            self._calls.cache.err = held["err"].data_ptr()
+        self.arrays = types.MappingProxyType(held)     # calls use these tensors: others cannot take their places
         self._workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
         torch.cuda.current_stream(dev).synchronize()   # ready for whichever stream comes first
 

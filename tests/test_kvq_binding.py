@@ -49,3 +49,31 @@ def test_data_on_another_device_than_the_arrays_is_refused(no_library):
     for call in calls(arrays(1), 1):      # the same calls with everything on one device go on
         with pytest.raises(AssertionError, match="reached"):
             call()
+
+
+@pytest.fixture
+def no_gpu_needed(monkeypatch):
+    """Allocations and waits of LowramKvq's constructor, without a GPU."""
+    zeros = torch.zeros
+
+    class Stream:
+        def synchronize(self):
+            pass
+
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: on_gpu(0, *a, **k) if device is not None else zeros(*a, **k))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
+
+
+def test_arrays_of_a_cache_cannot_be_exchanged(no_library, no_gpu_needed):
+    """Calls use the arrays that the cache was made with, so putting others in their place is refused."""
+    mine = arrays(0)
+    cache = K.LowramKvq(CFG, mine)
+    assert cache.arrays["table"] is mine["table"] and cache.arrays["k_mean"] is mine["k_mean"]
+    with pytest.raises(TypeError):
+        cache.arrays["table"] = on_gpu(0, 2, 2, dtype=torch.int32)
+    mine["table"] = None      # the caller's own dict is theirs
+    assert cache.arrays["table"] is not None
+    again = K.LowramKvq(CFG, cache.arrays)
+    assert all(again.arrays[n] is cache.arrays[n] for n in cache.arrays)
+    with pytest.raises(AssertionError, match="reached"):
+        K.lowram_kvq_write(CFG, cache.arrays, 0, *[on_gpu(0, 1, 2, 3, 2, 128)] * 2, on_gpu(0, 2, dtype=torch.int32))

@@ -878,7 +878,8 @@ class LowramKvq:
 
     ``cfg``: the fields of ``lowram_kvq_config``; ``arrays``: k_code, k_scale, v_code, v_scale and
     optionally k_mean and table (layouts of ``lowram.h``).  Without ``arrays`` they are allocated
-    on ``device``, with ``table`` as given (or none: sequence b owns pages b * max_pages + i).
+    on ``device``.  ``table``: where it is not among ``arrays`` (none at all: sequence b owns pages
+    b * max_pages + i).
     ``LowramKvq.arrays`` shows the tensors in use; write into them (a new table, say), a cache on other
     tensors is another ``LowramKvq``."""
 
@@ -890,10 +891,15 @@ class LowramKvq:
         if arrays is None:
             arrays = {n: torch.zeros(shape, dtype=dtype, device=device)
                       for n, (shape, dtype) in _kvq_layouts(c).items() if n not in ("table", "err")}
-            arrays["table"] = table
+
         def get(n):
             return arrays.get(n) if isinstance(arrays, (dict, types.MappingProxyType)) else getattr(arrays, n, None)
+
         held = {n: get(n) for n in _kvq_layouts(c)}
+        if table is not None:
+            if held["table"] is not None:
+                raise ValueError("table is given twice, among arrays and beside them")
+            held["table"] = table
         self._calls = _KvqPrepared(c, held)
         self.device = dev = held["k_code"].device
         if held["err"] is None:

@@ -77,3 +77,14 @@ def test_arrays_of_a_cache_cannot_be_exchanged(no_library, no_gpu_needed):
     assert all(again.arrays[n] is cache.arrays[n] for n in cache.arrays)
     with pytest.raises(AssertionError, match="reached"):
         K.lowram_kvq_write(CFG, cache.arrays, 0, *[on_gpu(0, 1, 2, 3, 2, 128)] * 2, on_gpu(0, 2, dtype=torch.int32))
+
+
+def test_table_beside_arrays(no_library, no_gpu_needed):
+    """``table`` completes arrays that have none; beside one of theirs it is refused, not ignored."""
+    table = on_gpu(0, 2, 2, dtype=torch.int32)
+    bare = {n: t for n, t in arrays(0).items() if n != "table"}
+    assert K.LowramKvq(CFG, bare, table=table).arrays["table"] is table
+    assert K.LowramKvq(CFG, bare).arrays["table"] is None
+    assert "table" not in bare
+    with pytest.raises(ValueError, match="table"):
+        K.LowramKvq(CFG, arrays(0), table=table)

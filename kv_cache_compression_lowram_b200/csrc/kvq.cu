@@ -26,7 +26,9 @@ lowram_status check(const lowram_kvq_config* c) {
   if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return inval("page must be 16, 32, 64, 128 or 256");
   if (c->max_pages > kMaxPagesSeq) return inval("max_pages exceeds 16384");
   if (c->batch > 65535 || c->n_kv_heads > 65535 || c->n_layers > 65535) return inval("batch, n_kv_heads and n_layers are at most 65535");
-  if ((uint64_t)c->n_layers * c->n_pages * c->n_kv_heads * c->page >= (1ull << 32))
+  // (the product of two of the sizes is below 2^47: the others are compared by division)
+  if ((uint64_t)c->n_layers * c->n_pages >= (1ull << 32) / ((uint64_t)c->n_kv_heads * c->page) + 1 ||
+      (uint64_t)c->n_layers * c->n_pages * c->n_kv_heads * c->page >= (1ull << 32))
     return inval("rows of the pool (n_layers * n_pages * n_kv_heads * page) must stay below 2^32");
   if (c->bits != 4 && c->bits != 8) return inval("bits must be 4 or 8");
   if (c->dtype != LOWRAM_F32 && c->dtype != LOWRAM_BF16) return inval("unknown dtype");

@@ -1,0 +1,22 @@
+"""What the C entry points of the quantised KV cache refuse before any CUDA call, beside the ordinary
+arguments."""
+
+import ctypes
+
+import pytest
+
+import kv_cache_compression_lowram_b200 as K
+from kvq_utils import config
+from test_kvq_host import PTR, attn_call, rows_call
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=1, layers=1 << 15, kv_heads=1 << 15, q_heads=1 << 15, n_pages=1 << 30, page=16, max_pages=1),
+    dict(batch=1, layers=1 << 15, kv_heads=1 << 14, q_heads=1 << 14, n_pages=1 << 30, page=32, max_pages=1)])
+def test_pools_whose_rows_pass_64_bits(kw):
+    """Products of sizes that are a multiple of 2^64 are not taken for a small pool."""
+    assert K.lowram_kvq_token_bytes(config(**kw)) == 0
+    with pytest.raises(K.LowramError):
+        K.lowram_kvq_workspace_bytes(config(**kw), 1, 1)
+    for fn in (K.lib().lowram_kvq_write, K.lib().lowram_kvq_read):
+        assert rows_call(fn, config(**kw)) == 1

@@ -16,6 +16,7 @@ lowram_status inval(const char* why) {
   return LOWRAM_EINVAL;
 }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 lowram_status check(const lowram_kvq_config* c) {
   if (!c) return inval("config is NULL");
@@ -47,7 +48,7 @@ lowram_status check_cache(const lowram_kvq_config* c, const lowram_kvq_cache* k,
   for (const void* p : need)
     if (!p || !aligned16(p)) return inval("a cache array is NULL or not 16-byte aligned");
   if (!aligned16(k->k_mean)) return inval("k_mean is not 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(k->table) | reinterpret_cast<uintptr_t>(k->err)) & 3) return inval("table or err is misaligned");
+  if (!aligned4(k->table) || !aligned4(k->err)) return inval("table or err is misaligned");
   if (!k->table && (int64_t)c->batch * c->max_pages > c->n_pages) return inval("without a table the pool needs batch * max_pages pages");
   if (layer0 < 0 || n_layers < 1 || layer0 > c->n_layers - n_layers) return inval("bad layer range");
   int lg = 4;
@@ -91,6 +92,7 @@ lowram_status rows_call(bool writes, const lowram_kvq_config* cfg, const lowram_
   if (n == 0) return LOWRAM_OK;
   a.n = n;
   if (!pos) return inval("pos is NULL");
+  if (!aligned4(pos) || !aligned4(count)) return inval("pos or count is misaligned");
   if ((st = check_rows(a, cfg->dtype, k, ks, !writes, &rk)) != LOWRAM_OK) return st;
   if ((st = check_rows(a, cfg->dtype, v, vs, !writes, &rv)) != LOWRAM_OK) return st;
   const long long pieces = ((n - 1) >> a.page_log2) + 2;
@@ -106,6 +108,7 @@ lowram_status check_attn(const lowram_kvq_config* cfg, const lowram_kvq_cache* c
   if (st != LOWRAM_OK) return st;
   if (n_q < 1 || n_q > kMaxQ) return inval("n_q must lie in [1, 16]");
   if (!q || !out || !lens || !aligned16(q) || !aligned16(out)) return inval("q, out or lens is NULL, or q or out not 16-byte aligned");
+  if (!aligned4(lens)) return inval("lens is misaligned");
   if ((long long)n_layers * a->B * a->Hkv * n_q >= (1LL << 27)) return inval("too many queries for one call: split the layers");
   a->n = n_q;
   return LOWRAM_OK;
@@ -163,6 +166,7 @@ lowram_status lowram_kvq_sparse_attn(const lowram_kvq_config* cfg, const lowram_
   if (st != LOWRAM_OK) return st;
   if (top_k < 1 || top_k > kMaxTopK) return inval("top_k must lie in [1, 512]");
   if (!a.k_mean) return inval("the cache has no k_mean");
+  if (!aligned4(sel)) return inval("sel is misaligned");
   return done(launch_sparse(a, cfg->dtype, top_k, q, lens, out, sel, reinterpret_cast<cudaStream_t>(stream)), "kvq sparse");
 }
 

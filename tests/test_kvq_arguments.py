@@ -20,3 +20,17 @@ def test_pools_whose_rows_pass_64_bits(kw):
         K.lowram_kvq_workspace_bytes(config(**kw), 1, 1)
     for fn in (K.lib().lowram_kvq_write, K.lib().lowram_kvq_read):
         assert rows_call(fn, config(**kw)) == 1
+
+
+MISPLACED = ctypes.c_void_p((1 << 20) + 2)      # no address of an int32
+
+
+def test_integers_at_odd_addresses():
+    """pos, count, lens and sel hold 32-bit integers: an address that is not a multiple of 4 would fault."""
+    for fn in (K.lib().lowram_kvq_write, K.lib().lowram_kvq_read):
+        for kw in (dict(pos=MISPLACED), dict(count=MISPLACED)):
+            assert rows_call(fn, **kw) == 1, kw
+            assert b"misaligned" in K.lib().lowram_last_error_string()
+    for sparse, kw in ((False, dict(lens=MISPLACED)), (True, dict(lens=MISPLACED)), (True, dict(sel=MISPLACED))):
+        assert attn_call(sparse, **kw) == 1, kw
+        assert b"misaligned" in K.lib().lowram_last_error_string()

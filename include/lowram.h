@@ -595,7 +595,8 @@ lowram_status lowram_kvq_read(const lowram_kvq_config* cfg, const lowram_kvq_cac
 uint64_t lowram_kvq_workspace_bytes(const lowram_kvq_config* cfg, int32_t n_layers, int32_t n_q);
 
 /* Attention of the last n_q tokens of every sequence over the sequence (causal among them):
- *   q, out  [n_layers][B][n_q][Hq][d] dt, DEVICE, 16-byte aligned; 1 <= n_q <= 16;
+ *   q, out  [n_layers][B][n_q][Hq][d] dt, DEVICE, 16-byte aligned; 1 <= n_q <= 16; out may be q
+ *           itself, but not overlap it otherwise;
  *   lens    [B] int32, DEVICE: tokens held by each sequence, its n_q query tokens included.
  * Query i attends tokens t < lens[b] - n_q + i + 1:  o = softmax_t(q . khat_t / sqrt(d)) vhat_t,
  * 0 for a query without tokens.  fp32 (or wider) logits, softmax statistics and sums; BF16

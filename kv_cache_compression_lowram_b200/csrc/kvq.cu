@@ -110,6 +110,9 @@ lowram_status check_attn(const lowram_kvq_config* cfg, const lowram_kvq_cache* c
   if (!q || !out || !lens || !aligned16(q) || !aligned16(out)) return inval("q, out or lens is NULL, or q or out not 16-byte aligned");
   if (!aligned4(lens)) return inval("lens is misaligned");
   if ((long long)n_layers * a->B * a->Hkv * n_q >= (1LL << 27)) return inval("too many queries for one call: split the layers");
+  const uint64_t bytes = (uint64_t)n_layers * a->B * n_q * a->Hq * a->d * (cfg->dtype == LOWRAM_F32 ? 4 : 2);
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  if (q0 != o0 && (q0 < o0 ? o0 - q0 : q0 - o0) < bytes) return inval("out overlaps q in part");
   a->n = n_q;
   return LOWRAM_OK;
 }

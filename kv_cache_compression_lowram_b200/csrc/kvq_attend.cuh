@@ -196,11 +196,11 @@ template <int BITS_, int D_, int ROWS_, bool F32_> struct Tile {
         if (j < rows) {
           const T* src = q_row(j) + lane * PER;
           constexpr int BY = PER * (int)sizeof(T);
-          if constexpr (BY == 4) *reinterpret_cast<uint32_t*>(raw[k]) = __ldg(reinterpret_cast<const uint32_t*>(src));
-          else if constexpr (BY == 8) *reinterpret_cast<uint2*>(raw[k]) = __ldg(reinterpret_cast<const uint2*>(src));
+          if constexpr (BY == 4) *reinterpret_cast<uint32_t*>(raw[k]) = __ldcg(reinterpret_cast<const uint32_t*>(src));
+          else if constexpr (BY == 8) *reinterpret_cast<uint2*>(raw[k]) = __ldcg(reinterpret_cast<const uint2*>(src));
           else
 #pragma unroll
-            for (int i = 0; i < BY / 16; ++i) reinterpret_cast<uint4*>(raw[k])[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            for (int i = 0; i < BY / 16; ++i) reinterpret_cast<uint4*>(raw[k])[i] = __ldcg(reinterpret_cast<const uint4*>(src) + i);
         }
       }
     }

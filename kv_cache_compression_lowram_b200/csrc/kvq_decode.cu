@@ -175,7 +175,7 @@ __device__ __forceinline__ void join_parts(const float* part, int c_first, int c
 
 template <int BITS, int D, int ROWS, bool F32>
 __global__ void __launch_bounds__(kThreads, Plan<BITS, D, ROWS, F32>::MINB)
-decode_kernel(Args a, int row_tiles, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
+decode_kernel(Args a, int row_tiles, const void* qv, const int32_t* __restrict__ lens, void* outv,
               unsigned* __restrict__ arrived, float* __restrict__ part) {
   using P = Plan<BITS, D, ROWS, F32>;
   using Tl = typename P::Tl;

@@ -243,7 +243,7 @@ template <class Score> __device__ __noinline__ void select_exactly(int n, int wa
 
 template <int BITS, int D, int ROWS, bool F32>
 __global__ void __launch_bounds__(kThreads, Plan<BITS, D, ROWS, F32>::MINB)
-sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __restrict__ qv, const int32_t* __restrict__ lens, void* __restrict__ outv,
+sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* qv, const int32_t* __restrict__ lens, void* outv,
               int32_t* __restrict__ sel) {
   using P = Plan<BITS, D, ROWS, F32>;
   using Tl = typename P::Tl;
@@ -301,7 +301,7 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* __r
         for (int r = 0; r < 4; ++r) {
           const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)min(j + r, a.g - 1) * D + c8 * 8);
 #pragma unroll
-          for (int k = 0; k < (int)sizeof(x[0]) / 16; ++k) reinterpret_cast<uint4*>(x[r])[k] = __ldg(src + k);
+          for (int k = 0; k < (int)sizeof(x[0]) / 16; ++k) reinterpret_cast<uint4*>(x[r])[k] = __ldcg(src + k);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r)

@@ -1,6 +1,7 @@
 """Calls of the quantised KV cache on the GPU beside the ordinary ones: other streams, in place, several
 threads."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -62,3 +63,19 @@ def test_validate_waits_for_calls_on_other_streams():
             torch.cuda._sleep(LONG)
         call()
         assert cache.validate() == 2 and cache.validate() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,group,n,lens", [(128, 4, 1, [9000, 0, 33]), (64, 16, 4, [3000, 5, 700]), (256, 12, 3, [2000, 64, 1])])
+def test_attention_in_place(dtype, d, group, n, lens):
+    """out = q, also where several blocks share a sequence and where its rows take more than one tile."""
+    cfg = config(batch=3, layers=2, kv_heads=2, q_heads=2 * group, head_dim=d, page=16, max_pages=-(-max(lens) // 16), n_pages=60, dtype=dtype)
+    arrays = fill(dict(cfg, batch=1, max_pages=1), 42)
+    arrays["table"] = np.random.default_rng(3).integers(0, 60, (3, cfg["max_pages"])).astype(np.int32)
+    cache = K.LowramKvq(cfg, to_device(arrays), max_q=n)
+    q, lens = queries(cfg, n).to(DEV), i32(lens)
+    for call in (lambda q, out: cache.decode(q, lens, out=out), lambda q, out: cache.decode_sparse(q, lens, 40, out=out)):
+        want = call(q, None)
+        for _ in range(3):
+            own = q.clone()
+            assert call(own, own) is own and torch.equal(own, want)

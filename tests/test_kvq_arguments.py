@@ -34,3 +34,18 @@ def test_integers_at_odd_addresses():
     for sparse, kw in ((False, dict(lens=MISPLACED)), (True, dict(lens=MISPLACED)), (True, dict(sel=MISPLACED))):
         assert attn_call(sparse, **kw) == 1, kw
         assert b"misaligned" in K.lib().lowram_last_error_string()
+
+
+def test_outputs_that_overlap_the_queries_in_part():
+    """out may be q itself (a row is read before it is written), but not a shifted view of it."""
+    size = 2 * 8 * 128 * 2      # config()'s batch, query heads, channels, bytes
+    for sparse in (False, True):
+        for shift in (16, 256, size - 16):
+            for q, out in ((PTR.value, PTR.value + shift), (PTR.value + shift, PTR.value)):
+                assert attn_call(sparse, q=ctypes.c_void_p(q), out=ctypes.c_void_p(out)) == 1
+                assert b"overlaps" in K.lib().lowram_last_error_string()
+        # itself, and neighbours: refused for something else
+        for out in (PTR.value, PTR.value + size):
+            kw = dict(top_k=0) if sparse else dict(ws=None)
+            assert attn_call(sparse, out=ctypes.c_void_p(out), **kw) == 1
+            assert b"overlaps" not in K.lib().lowram_last_error_string()

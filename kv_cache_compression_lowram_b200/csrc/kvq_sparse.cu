@@ -19,6 +19,8 @@
 #include <cooperative_groups.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "kvq.cuh"
 #include "kvq_attend.cuh"
 
@@ -613,7 +615,14 @@ sparse_kernel(Args a, int top_k, int share_room, int score_room, const void* qv,
 template <int BITS, int D, int ROWS, bool F32>
 cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, void* out, int32_t* sel, cudaStream_t s) {
   using P = Plan<BITS, D, ROWS, F32>;
-  static int fits[64][4] = {{0}};   // per device: clusters of 1, 2, 4, 8 CTAs resident at once, plus one
+  // per device: clusters of 1, 2, 4, 8 CTAs resident at once, where an SM holds one CTA and where it
+  // holds as many as the registers allow
+  struct Fits {
+    std::atomic<bool> known{false};
+    std::atomic<int> clusters[2][4] = {};
+    std::atomic<int> per_sm{0}, beside{0};   // shared memory of an SM, and of a CTA beside its dynamic one
+  };
+  static Fits fits[64];
   auto kernel = sparse_kernel<BITS, D, ROWS, F32>;
   const unsigned units = (unsigned)a.n_layers * a.B * a.n * a.Hkv;
   int dev = 0;
@@ -634,28 +643,35 @@ cudaError_t go(const Args& a, int top_k, const void* q, const int32_t* lens, voi
   auto smem_of = [&](int cs) {
     return (score_room(cs) > P::ATTEND ? score_room(cs) : P::ATTEND) + (a.max_pages + 31) / 32 * 4 + top_k * 4 + P::SMALL + 16;
   };
-  int now[4];
-  int* fit = dev < 64 ? fits[dev] : now;
-  if (dev >= 64 || !fit[0]) {
-    int room = 0, found[4];
+  Fits now;
+  Fits& fit = dev < 64 ? fits[dev] : now;
+  if (!fit.known) {   // (threads that come here at once write the same numbers)
+    int room = 0, per_sm = 0, reserved = 0;
     if ((e = cudaDeviceGetAttribute(&room, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess) return e;
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room - (int)fa.sharedSizeBytes)) != cudaSuccess) return e;
-    cfg.dynamicSmemBytes = P::ATTEND + 4096 + P::SMALL;
-    for (int k = 0; k < 4; ++k) {
-      cfg.gridDim = 1 << k;
-      attr.val.clusterDim.x = 1 << k;
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      int n = 0;
-      if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
-      found[k] = n + 1;
+    room -= (int)fa.sharedSizeBytes;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room)) != cudaSuccess) return e;
+    for (int many = 0; many < 2; ++many) {
+      cfg.dynamicSmemBytes = many ? P::ATTEND + P::SMALL + 16 : room;
+      for (int k = 0; k < 4; ++k) {
+        cfg.gridDim = 1 << k;
+        attr.val.clusterDim.x = 1 << k;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+        fit.clusters[many][k] = n;
+      }
     }
-    for (int k = 3; k >= 0; --k) fit[k] = found[k];
+    fit.per_sm = per_sm;
+    fit.beside = (int)fa.sharedSizeBytes + reserved;
+    fit.known = true;
   }
   // the largest cluster that leaves all units resident at once
   int k = 3;
-  while (k > 0 && (int)units > (fit[k] - 1)) --k;
+  while (k > 0 && units > (unsigned)fit.clusters[P::MINB * (smem_of(1 << k) + fit.beside) <= fit.per_sm][k]) --k;
   const int cs = 1 << k;
   cfg.dynamicSmemBytes = smem_of(cs);
   cfg.gridDim = units * cs;

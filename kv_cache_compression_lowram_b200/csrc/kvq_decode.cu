@@ -11,6 +11,8 @@
 // cp.async fills ahead, across unit borders; at the end of a unit's part they join their sums.
 // A unit that several CTAs share is joined by the one that finishes last, in the order of the
 // pieces (the result does not depend on which that is).
+#include <atomic>
+
 #include "kvq.cuh"
 #include "kvq_attend.cuh"
 
@@ -487,11 +489,11 @@ template <int BITS, int D, int ROWS, bool F32>
 cudaError_t go(const Args& a, const void* q, const int32_t* lens, void* out, void* ws, cudaStream_t s) {
   using P = Plan<BITS, D, ROWS, F32>;
   // per device: the kernel's attribute and the CTAs that are resident at once
-  static int workers[64] = {0};
+  static std::atomic<int> workers[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int w = dev < 64 ? workers[dev] : 0;
+  int w = dev < 64 ? workers[dev].load() : 0;
   if (!w) {
     int sm = 0, per = 0;
     if ((e = cudaFuncSetAttribute(decode_kernel<BITS, D, ROWS, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM)) != cudaSuccess) return e;

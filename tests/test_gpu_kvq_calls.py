@@ -1,15 +1,20 @@
 """Calls of the quantised KV cache on the GPU beside the ordinary ones: other streams, in place, several
 threads."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import kv_cache_compression_lowram_b200 as K
-from kvq_utils import config, fill, queries, to_device
+from kvq_utils import check_attention, config, fill, queries, to_device
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LONG = 200_000_000      # cycles: about a tenth of a second
 
 
@@ -79,3 +84,48 @@ def test_attention_in_place(dtype, d, group, n, lens):
         for _ in range(3):
             own = q.clone()
             assert call(own, own) is own and torch.equal(own, want)
+
+
+def test_first_calls_of_several_threads():
+    """The first calls of a process, made by several threads at once, each with its cache and stream."""
+    code = """
+import threading, torch, kv_cache_compression_lowram_b200 as K
+N = 6
+cfg = dict(batch=2, n_layers=1, n_kv_heads=2, n_q_heads=8, head_dim=128, page=16, n_pages=64, max_pages=32, bits=4, dtype="bf16")
+torch.manual_seed(1)
+x = torch.randn(1, 2, 500, 2, 128, device="cuda").bfloat16()
+q = torch.randn(1, 2, 1, 8, 128, device="cuda").bfloat16()
+pos, lens = (torch.full((2,), n, dtype=torch.int32, device="cuda") for n in (0, 500))
+caches, streams = [K.LowramKvq(cfg) for _ in range(N)], [torch.cuda.Stream() for _ in range(N)]
+outs, gate = [None] * N, threading.Barrier(N)
+torch.cuda.synchronize()
+def work(i):
+    gate.wait()
+    with torch.cuda.stream(streams[i]):
+        caches[i].write(x, x, pos)
+        outs[i] = [caches[i].decode(q, lens), caches[i].decode_sparse(q, lens, 9)] + list(caches[i].read(pos, n=500))
+threads = [threading.Thread(target=work, args=(i,)) for i in range(N)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for o in outs for a, b in zip(o, outs[0])) and torch.isfinite(outs[0][0]).all()
+assert (outs[0][2] - x).abs().max() < 0.5 and all(c.validate() == 0 for c in caches)
+print("threads done")
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "threads done" in done.stdout, done.stderr[-2000:]
+
+
+@pytest.mark.parametrize("batch,pages", [(1, 9000), (3, 9000), (24, 6000), (4, 5200)])
+def test_sparse_clusters_of_every_size(batch, pages):
+    """Tables so wide that an SM holds one block: clusters of 8, 4, 2 and 1 blocks, all with the same pages
+    selected as among the same keys in the oracle."""
+    r = np.random.default_rng(batch)
+    lens = [pages * 16] + [int(x) for x in r.integers(1, 4000, batch - 1)]
+    cfg = config(batch=batch, kv_heads=8, q_heads=16, head_dim=64, page=16, max_pages=pages, n_pages=200)
+    arrays = fill(dict(cfg, batch=1, max_pages=1), 43)
+    arrays["table"] = r.integers(0, 200, (batch, pages)).astype(np.int32)
+    cache = K.LowramKvq(cfg, to_device(arrays))
+    q = queries(cfg, seed=5)
+    out, sel = cache.decode_sparse(q.to(DEV), i32(lens), 20, sel=True)
+    check_attention(cfg, arrays, q, lens, out, top_k=20, sel=sel)

@@ -516,8 +516,8 @@ lowram_status lowram_encode(const lowram_config* cfg, int32_t n_resid, const voi
  *     lo = fp16(min x),   s = fp16(fp32((max x - min x) / (2^b - 1))),
  *     n  = clamp(round-half-even((x - lo) / s), 0, 2^b - 1)   (n = 0 when s = 0),
  *     and the group stands for  xhat = lo + s * n.
- * Values must be finite and within fp16's range: a group that holds another value reads back
- * as non-finite values (it does not disturb other groups).
+ * Values must be finite, and a group's smallest value and its s within fp16's range: a group for
+ * which that does not hold reads back as non-finite values (it does not disturb other groups).
  *
  * A pool holds n_pages pages of `page` tokens for every layer; sequence b's i-th page is
  * table[b][i], the same for all layers (table NULL: page b * max_pages + i).  Sequences may

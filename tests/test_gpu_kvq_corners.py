@@ -248,3 +248,18 @@ def test_write_odd_values_bf16(bits):
     x[~clean] = 0
     codes, scale = O.quantise(x.bfloat16().double().numpy(), bits)
     assert torch.equal(got[clean], torch.tensor(O.dequantise(codes, scale)).float().bfloat16()[clean])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_beyond_fp16(bits, dtype):
+    """A group's largest value may pass fp16's range as long as its offset and step do not; where one of
+    them does, the whole group is non-finite, and the next one is not."""
+    d, q = 128, (1 << bits) - 1
+    r = torch.rand(4, d, generator=torch.Generator().manual_seed(2))
+    r[:, ::64] = 0      # the smallest value of each group
+    check_rows(torch.stack([r[0] * 60000.0 * q, 6.5e4 * (2 * r[1] - 1), r[2] * 6.5e4 * q - 6.5e4]), bits, d, dtype)
+    x = torch.stack([r[0] * 90000.0 * q, r[1] - 7e4, -1e6 * r[2], 1e5 + r[3]])
+    x[:, 64:] = r[:, 64:]
+    back = written_rows(x, bits, d, dtype)[2]
+    assert not torch.isfinite(back[:, :64]).any() and torch.isfinite(back[:, 64:]).all()

@@ -582,7 +582,7 @@ lowram_status lowram_kvq_write(const lowram_kvq_config* cfg, const lowram_kvq_ca
                                const void* v, const int64_t* v_stride, const int32_t* pos, const int32_t* count,
                                lowram_stream stream);
 
-/* Read tokens back: k_out, v_out take xhat (rounded once to dt) of tokens pos[b] + i,
+/* Read tokens back: k_out, v_out take xhat (in fp32, then rounded to dt) of tokens pos[b] + i,
  * i < min(count[b], n_tok), addressed like k and v of lowram_kvq_write (strides of axes longer
  * than one may not be 0); the rows behind are left as they were. */
 lowram_status lowram_kvq_read(const lowram_kvq_config* cfg, const lowram_kvq_cache* cache, int32_t layer0,
@@ -599,8 +599,10 @@ uint64_t lowram_kvq_workspace_bytes(const lowram_kvq_config* cfg, int32_t n_laye
  *           itself, but not overlap it otherwise;
  *   lens    [B] int32, DEVICE: tokens held by each sequence, its n_q query tokens included.
  * Query i attends tokens t < lens[b] - n_q + i + 1:  o = softmax_t(q . khat_t / sqrt(d)) vhat_t,
- * 0 for a query without tokens.  fp32 (or wider) logits, softmax statistics and sums; BF16
- * calls round the softmax weights to fp16 (times the value scale) for the tensor cores.
+ * 0 for a query without tokens.  fp32 (or wider) logits, softmax statistics and sums.  For the
+ * tensor cores, BF16 calls round the softmax weights (times the value scale) to fp16 and lose digits
+ * of query entries below 2^-27 of their row's largest; F32 calls hold queries and weights as two
+ * fp16 numbers, 22 bits.
  * workspace: lowram_kvq_workspace_bytes bytes, 16-byte aligned, all zero before its first use;
  * a call leaves it ready for the next one.  Calls that overlap on the GPU need workspaces of
  * their own. */

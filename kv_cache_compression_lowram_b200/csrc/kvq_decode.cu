@@ -1,12 +1,12 @@
 // Quantised KV cache: attention of the last tokens over whole sequences.
 //
 // Bound by HBM: 2 (d bits / 8 + d / 16) bytes per cached token and KV head, read once per 4, 8 or 16
-// query rows (4 layers of 4 x 32K tokens, 8 heads of 128 in 4 bits: 604 MB in 130 us, 4.6 TB/s, 71 % of the
-// measured copy rate; a further such layer costs 28.7 us, 5.3 TB/s) -- and, nearly as much, by the
-// instructions that unpack (48 % of the issue slots).  All steps of all units -- a unit is (sequence, layer, KV head, tile of query rows), a
-// step 16 or 32 of its tokens -- form one line that is shared out evenly among the CTAs (one wave of
-// them), so ragged lengths and few long sequences load the SMs alike without the host knowing a
-// length.
+// query rows (4 layers of 4 x 32K tokens, 8 heads of 128 in 4 bits: 604 MB in 129 us from a CUDA graph, 4.7 TB/s,
+// 72 % of the measured copy rate, and 134 to 140 us a Python call, depending on the machine; one layer 42 us,
+// a further one 29) -- and, nearly as much, by the instructions that unpack (49 % of the issue slots).
+// All steps of all units -- a unit is (sequence, layer, KV head, tile of query rows), a step 16 or 32 of
+// its tokens -- form one line that is shared out evenly among the CTAs (one wave of them), so ragged
+// lengths and few long sequences load the SMs alike without the host knowing a length.
 // A CTA's four warps take its steps in turn, each through a ring of its own in shared memory that
 // cp.async fills ahead, across unit borders; at the end of a unit's part they join their sums.
 // A unit that several CTAs share is joined by the one that finishes last, in the order of the
@@ -28,6 +28,11 @@ constexpr int kMaxWorkers = 640;
 // parts of 8 steps, 8 us whole).  A part has at least kLeast steps.  A unit's queries and its
 // joining cost a CTA about as much as kOver steps: on the line every unit is so much longer.
 // (16 ragged sequences, some of a few tokens: 128 us with 0, 68 with 6, 58 with 10 and with 16.)
+// The steps of other shapes cost more or less than those, and the same numbers suit them: 64 ragged
+// sequences of 128 in 4 bits take 40.7, 39.2 and 43.3 us with kOver 6, 12 and 24, 40 of 64 in fp32 22.3, 21.7
+// and 24.7; with kWhole 8, 16 and 32, 250 tokens of 256 in 8 bits 15.5, 13.3 and 13.3, 700 of 128 in 4 bits
+// 10.0, 10.0 and 11.3; with kSpare 4 and 12, 16 ragged sequences of 128 in 4 bits 26.2 and 28.4, of 64 22.8 and 21.9.
+// (Equal parts are tried for up to 32 sequences: a lane each.)
 constexpr unsigned kWhole = 16, kLeast = 8, kSpare = 12, kOver = 12;
 constexpr size_t kPartBytes = (size_t)2 * kMaxWorkers * 16 * (128 + 2) * 4;   // two parts per CTA; 8 rows of 256 + 2 are fewer
 
@@ -40,7 +45,8 @@ template <int BITS, int D, int ROWS, bool F32> struct Plan {
   static constexpr int RING = kWarps * STAGES * SLOT;
   static constexpr int SMEM = RING + JOIN + Tl::QFRAG + Tl::QMETA + (kWarps + 1) * Tl::ROWS * 8 + 16;
   // Three CTAs an SM where the shared memory allows it (d = 128 in 4 bits, four rows: 12 warps of 168
-  // registers; two CTAs of 255 took 21 % longer, four of 128 11 %, and steps of 16 tokens 17 %).
+  // registers, a few of which are kept in memory over a step -- 64 bytes stored, 52 loaded a thread, 192 and
+  // 172 with eight rows; two CTAs of 255 took 21 % longer, four of 128 11 %, and steps of 16 tokens 17 %).
   static constexpr int MINB = SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);
 };
 

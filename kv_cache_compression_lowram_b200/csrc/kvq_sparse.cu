@@ -12,10 +12,11 @@
 //      more in fp64 and ranked by comparison;
 //   3. the selected pages' 16-token blocks go round the warps of the cluster, as in the attention
 //      over whole sequences; CTAs join their sums and the cluster joins the CTAs'.
-// No workspace, no second launch, and nothing is written but the outputs.  One 128K sequence, 32 of 2048
+// No workspace, no second launch, and nothing is written but the outputs.  (d = 128 in 4 bits, four rows: two
+// CTAs an SM, 128 registers, and 48 bytes a thread stored to memory and 84 loaded.)  One 128K sequence, 32 of 2048
 // pages of 64: 20 us, of which the histogram and the ranks take 5, the gathering of scores and the
-// queries 2 each, scoring 3, attention 2.  16 sequences of up to 64K, 2 layers: 47 us for 109 MB,
-// 2.3 TB/s: the longest sequence's steps in a row, half of it attention at the rate of whole sequences.
+// queries 2 each, scoring 3, attention 2.  16 sequences of up to 64K, 2 layers: 45 us for 109 MB,
+// 2.4 TB/s: the longest sequence's steps in a row, half of it attention at the rate of whole sequences.
 #include <cooperative_groups.h>
 #include <limits.h>
 
